@@ -21,12 +21,18 @@ LIB_PATH = os.path.join(_PKG, "libgdr2.so")
 GDR2_OK, GDR2_ERR_INVALID_ARG, GDR2_ERR_UNSUPPORTED, GDR2_ERR_CUDA, GDR2_ERR_TIMEOUT = range(5)
 GDR2_F32, GDR2_BF16 = 0, 1
 CHUNK = 64
+SSM_CHUNK = 16  # GDR2_SSM_CHUNK
 _STATUS_NAMES = {0: "OK", 1: "INVALID_ARG", 2: "UNSUPPORTED", 3: "CUDA", 4: "TIMEOUT"}
 
 # Every symbol include/gdr2.h declares (the ABI tests check the exports).
 EXPORTED_SYMBOLS = ("gdr2_abi_version", "gdr2_last_error", "gdr2_forward_workspace_bytes", "gdr2_forward",
                     "gdr2_forward_gated", "gdr2_forward_varlen_workspace_bytes", "gdr2_forward_varlen",
                     "gdr2_forward_ex", "gdr2_short_conv_silu", "gdr2_gate_activations", "gdr2_segment_states",
+                    "gdr2_short_conv_silu_backward_workspace_bytes", "gdr2_short_conv_silu_backward",
+                    "gdr2_ssm_scan_workspace_bytes", "gdr2_ssm_scan", "gdr2_ssm_step",
+                    "gdr2_ssm_scan_backward_workspace_bytes", "gdr2_ssm_scan_backward",
+                    "gdr2_head_norm_rope", "gdr2_head_norm_rope_backward_workspace_bytes",
+                    "gdr2_head_norm_rope_backward",
                     "gdr2_decode_step", "gdr2_decode_step_gated",
                     "gdr2_backward_workspace_bytes", "gdr2_backward", "gdr2_backward_gated", "gdr2_backward_noalloc",
                     "gdr2_sync_status", "gdr2_debug_force_timeout", "gdr2_debug_recip",
@@ -75,6 +81,29 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
         lib.gdr2_short_conv_silu.argtypes = [I] * 7 + [ctypes.c_float] + [P] * 7
         lib.gdr2_gate_activations.restype = I
         lib.gdr2_gate_activations.argtypes = [I] + [ctypes.c_longlong, P, P] * 3 + [P]
+        F, LL = ctypes.c_float, ctypes.c_longlong
+        lib.gdr2_short_conv_silu_backward_workspace_bytes.restype = Z
+        lib.gdr2_short_conv_silu_backward_workspace_bytes.argtypes = [I] * 5
+        lib.gdr2_short_conv_silu_backward.restype = I
+        lib.gdr2_short_conv_silu_backward.argtypes = [I] * 7 + [F] + [P] * 9 + [Z, P]
+        ssm_in = [P, LL, P, LL, P, P, LL, P, LL, P, P, LL, P]  # x, step, A, Bm, Cm, Dskip, z, step_bias
+        lib.gdr2_ssm_scan_workspace_bytes.restype = Z
+        lib.gdr2_ssm_scan_workspace_bytes.argtypes = [I] * 4
+        lib.gdr2_ssm_scan.restype = I
+        lib.gdr2_ssm_scan.argtypes = [I] * 6 + [P] + ssm_in + [P] * 5 + [Z, P]
+        lib.gdr2_ssm_step.restype = I
+        lib.gdr2_ssm_step.argtypes = [I] * 5 + ssm_in + [P] * 3
+        lib.gdr2_ssm_scan_backward_workspace_bytes.restype = Z
+        lib.gdr2_ssm_scan_backward_workspace_bytes.argtypes = [I] * 5
+        lib.gdr2_ssm_scan_backward.restype = I
+        lib.gdr2_ssm_scan_backward.argtypes = [I] * 6 + ssm_in + [P] * 14 + [Z, P]
+        rope_in = [I] * 7 + [F, P, LL, P, LL, P, P, I, I, P, I, P, I]
+        lib.gdr2_head_norm_rope.restype = I
+        lib.gdr2_head_norm_rope.argtypes = rope_in + [P] * 3
+        lib.gdr2_head_norm_rope_backward_workspace_bytes.restype = Z
+        lib.gdr2_head_norm_rope_backward_workspace_bytes.argtypes = [I]
+        lib.gdr2_head_norm_rope_backward.restype = I
+        lib.gdr2_head_norm_rope_backward.argtypes = rope_in + [P] * 7 + [Z, P]
         lib.gdr2_segment_states.restype = I
         lib.gdr2_segment_states.argtypes = [I] * 5 + [P] * 6
         lib.gdr2_forward_gated.restype = I
@@ -407,6 +436,263 @@ def gdr2_block_prologue(xq, xk, xv, conv_q, conv_k, conv_v, a, b, w, *, states=N
     v, nv = gdr2_short_conv_silu(xv, conv_v, sv, l2norm=False, **kw)
     la, bo, wo = gdr2_gate_activations(a, b, w, stream=stream)
     return q, k, v, la, bo, wo, ((nq, nk, nv) if final_state else None)
+
+
+@_one_device
+def gdr2_short_conv_silu_backward(x, weight, dy, state=None, dstate_out=None, *, l2norm=False, eps=1e-6,
+                                  want_dstate=None, workspace=None, stream=None):
+    """Gradients of gdr2_short_conv_silu over dense sequences: of <y, dy> + <state_out, dstate_out>.
+
+    x, dy: [N, T, H, d]; weight [H * d, W] fp32 (or [H * d, 1, W]); state, dstate_out:
+    [N, W - 1, H, d] in x's dtype or None. Returns dict dx, dweight (weight's shape, fp32) and
+    dstate (by default when a state is given, else None).
+    """
+    lib = load_library()
+    N, T, H, d = x.shape
+    wgt = weight.reshape(weight.shape[0], weight.shape[-1]) if weight.dim() == 3 else weight
+    W = int(wgt.shape[-1])
+    dt = x.dtype
+    _check(x, "x", (N, T, H, d), dt)
+    _check(dy, "dy", (N, T, H, d), dt)
+    _check(wgt, "weight", (H * d, W), torch.float32)
+    _check(state, "state", (N, W - 1, H, d), dt)
+    _check(dstate_out, "dstate_out", (N, W - 1, H, d), dt)
+    want = state is not None if want_dstate is None else want_dstate
+    g = {"dx": torch.empty_like(x), "dweight": torch.empty(tuple(weight.shape), dtype=torch.float32, device=x.device),
+         "dstate": torch.empty((N, W - 1, H, d), dtype=dt, device=x.device) if want else None}
+    if N * H == 0:
+        g["dweight"].zero_()
+    need = lib.gdr2_short_conv_silu_backward_workspace_bytes(N, T, H, d, W)
+    workspace = _workspace(workspace, need, x.device)
+    st = lib.gdr2_short_conv_silu_backward(N, T, H, d, _dt(x), W, int(bool(l2norm)), ctypes.c_float(eps), _some(x),
+                                           _some(wgt), _some(state), _some(dy), _some(dstate_out), _some(g["dx"]),
+                                           _some(g["dweight"]), _some(g["dstate"]), _some(workspace),
+                                           _nbytes(workspace), _stream(stream))
+    _raise(lib, st)
+    return g
+
+
+def _some(t):
+    """The data pointer, or NULL for None and for a tensor without elements."""
+    return None if t is None or t.numel() == 0 else _ptr(t)
+
+
+def _nbytes(t):
+    return ctypes.c_size_t(0 if t is None else t.numel() * t.element_size())
+
+
+def _workspace(given, need, device):
+    """The caller's workspace, or one of `need` bytes (None when nothing is needed)."""
+    if given is not None:
+        if not given.is_cuda or not given.is_contiguous():
+            raise ValueError("workspace must be a contiguous CUDA tensor")
+        return given
+    return torch.empty(need, dtype=torch.uint8, device=device) if need > 0 else None
+
+
+def _rows(t, name, lead, width, dtype):
+    """Checks a token tensor [*lead, width] whose rows may be views of a wider one (the last
+    dimension dense, the same distance between all rows); returns that distance in elements."""
+    if t is None:
+        return 0
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if tuple(t.shape) != (*lead, width):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(*lead, width)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.numel() == 0:
+        return width
+    if width > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must be dense in its last dimension")
+    ld, rows = None, 1  # distance between rows; the rows that the dimensions from here on hold
+    for n, s in reversed(list(zip(lead, t.stride()[:-1]))):
+        if n > 1:
+            ld = s if ld is None else ld
+            if s != ld * rows:
+                raise ValueError(f"the rows of {name} must all be the same distance apart")
+        rows *= n
+    ld = width if ld is None else ld
+    if ld < width:
+        raise ValueError(f"the rows of {name} overlap")
+    return ld
+
+
+def _ssm_inputs(x, dt, A, Bm, Cm, D, z, dt_bias, packed=None):
+    """Checks the inputs that the scan, its step and its backward share; returns their sizes
+    and the C arguments x .. step_bias."""
+    lead, C = tuple(x.shape[:-1]), x.shape[-1]
+    N = A.shape[-1]
+    t = x.dtype
+    lds = [_rows(v, n, lead, w, t) for v, n, w in ((x, "x", C), (dt, "dt", C), (Bm, "Bm", N), (Cm, "Cm", N),
+                                                    (z, "z", C))]
+    _check(A, "A", (C, N), torch.float32)
+    _check(D, "D", (C,), torch.float32)
+    _check(dt_bias, "dt_bias", (C,), torch.float32)
+    if packed is not None:
+        _check_cu_seqlens(packed, x.device)
+    for v, n in ((dt, "dt"), (A, "A"), (Bm, "Bm"), (Cm, "Cm"), (D, "D"), (z, "z"), (dt_bias, "dt_bias")):
+        if v is not None and v.device != x.device:
+            raise ValueError(f"{n} must be on x's device")
+    args = [_some(x), lds[0], _some(dt), lds[1], _some(A), _some(Bm), lds[2], _some(Cm), lds[3], _some(D), _some(z),
+            lds[4], _some(dt_bias)]
+    return lead, C, N, t, args
+
+
+@_one_device
+def gdr2_ssm_scan(x, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, S0=None, *, softplus=True, cu_seqlens=None,
+                  final_state=True, save_states=False, out=None, workspace=None, stream=None):
+    """Selective state-space scan over whole sequences. Returns (y, S_T, saved_states).
+
+    h_t = exp(s_t A) h_{t-1} + s_t Bm_t x_t with s_t = softplus(dt_t + dt_bias) (softplus=False:
+    dt_t + dt_bias); y_t = (Cm_t . h_t + D x_t) * silu(z_t).
+    x, dt, z: [B, T, C]; Bm, Cm: [B, T, N] (one dtype, fp32 or bf16; views of fused projections
+    keep their row stride); with cu_seqlens (int32 [B + 1]) [T, .], packed. A: [C, N], D, dt_bias:
+    [C], S0, S_T: [B, C, N] fp32; N is 8, 16, 32 or 64. saved_states, when asked for (dense):
+    [B, ceil(T / 16), C, N], for gdr2_ssm_scan_backward.
+    """
+    lib = load_library()
+    if x.dim() != (2 if cu_seqlens is not None else 3):
+        raise ValueError("x must be [B, T, C], or [T, C] with cu_seqlens")
+    lead, C, N, t, args = _ssm_inputs(x, dt, A, Bm, Cm, D, z, dt_bias, cu_seqlens)
+    T = lead[-1]
+    B = lead[0] if cu_seqlens is None else cu_seqlens.numel() - 1
+    dev = x.device
+    _check(S0, "S0", (B, C, N), torch.float32)
+    y = out if out is not None else torch.empty((*lead, C), dtype=t, device=dev)
+    _check(y, "out", (*lead, C), t)
+    S_T = torch.empty((B, C, N), dtype=torch.float32, device=dev) if final_state else None
+    if save_states and cu_seqlens is not None:
+        raise ValueError("save_states is for dense sequences (the backward takes no cu_seqlens)")
+    saved = torch.empty((B, -(-T // SSM_CHUNK), C, N), dtype=torch.float32, device=dev) if save_states else None
+    need = lib.gdr2_ssm_scan_workspace_bytes(B if cu_seqlens is None else 1, T, C, N)
+    workspace = _workspace(workspace, need, dev)
+    st = lib.gdr2_ssm_scan(B, T, C, N, _dt(x), int(bool(softplus)), _ptr(cu_seqlens), *args, _some(S0), _some(y),
+                           _some(S_T), _some(saved), _some(workspace), _nbytes(workspace), _stream(stream))
+    _raise(lib, st)
+    return y, S_T, saved
+
+
+@_one_device
+def gdr2_ssm_step(x, dt, A, Bm, Cm, S, D=None, z=None, dt_bias=None, *, softplus=True, out=None, stream=None):
+    """One token of gdr2_ssm_scan for B resident states: x, dt, z [B, C], Bm, Cm [B, N]; S
+    [B, C, N] fp32 is updated in place. Returns y [B, C]."""
+    lib = load_library()
+    lead, C, N, t, args = _ssm_inputs(x, dt, A, Bm, Cm, D, z, dt_bias)
+    if len(lead) != 1:
+        raise ValueError("x must be [B, C]")
+    _check(S, "S", (*lead, C, N), torch.float32)
+    y = out if out is not None else torch.empty((*lead, C), dtype=t, device=x.device)
+    _check(y, "out", (*lead, C), t)
+    st = lib.gdr2_ssm_step(lead[0], C, N, _dt(x), int(bool(softplus)), *args, _some(S), _some(y), _stream(stream))
+    _raise(lib, st)
+    return y
+
+
+@_one_device
+def gdr2_ssm_scan_backward(x, dt, A, Bm, Cm, dy, D=None, z=None, dt_bias=None, S0=None, dS_T=None, saved_states=None,
+                           *, softplus=True, want_dS0=True, workspace=None, stream=None):
+    """Gradients of <y, dy> + <S_T, dS_T> of the dense gdr2_ssm_scan. Returns dict dx, ddt, dBm, dCm
+    (x's dtype), dA, dD, ddt_bias, dS0 (fp32) and dz; those of absent inputs are None (dS0 by want_dS0).
+    Without saved_states the states are formed again."""
+    lib = load_library()
+    if x.dim() != 3:
+        raise ValueError("x must be [B, T, C]")
+    (B, T), C, N, t, args = _ssm_inputs(x, dt, A, Bm, Cm, D, z, dt_bias)
+    dev = x.device
+    _check(dy, "dy", (B, T, C), t)
+    _check(S0, "S0", (B, C, N), torch.float32)
+    _check(dS_T, "dS_T", (B, C, N), torch.float32)
+    _check(saved_states, "saved_states", (B, -(-T // SSM_CHUNK), C, N), torch.float32)
+    f32 = lambda *s: torch.empty(s, dtype=torch.float32, device=dev)  # noqa: E731
+    own = lambda *s: torch.empty(s, dtype=t, device=dev)  # noqa: E731
+    g = {"dx": own(B, T, C), "ddt": own(B, T, C), "dA": f32(C, N), "dBm": own(B, T, N), "dCm": own(B, T, N),
+         "dD": None if D is None else f32(C), "dz": None if z is None else own(B, T, C),
+         "ddt_bias": None if dt_bias is None else f32(C), "dS0": f32(B, C, N) if want_dS0 else None}
+    need = lib.gdr2_ssm_scan_backward_workspace_bytes(B, T, C, N, int(saved_states is not None))
+    workspace = _workspace(workspace, need, dev)
+    st = lib.gdr2_ssm_scan_backward(B, T, C, N, _dt(x), int(bool(softplus)), *args, _some(S0), _some(dy), _some(dS_T),
+                                    _some(saved_states), *(_some(g[k]) for k in ("dx", "ddt", "dA", "dBm", "dCm", "dD",
+                                                                                 "dz", "ddt_bias", "dS0")),
+                                    _some(workspace), _nbytes(workspace), _stream(stream))
+    _raise(lib, st)
+    return g
+
+
+_NORMS = {None: 0, "rms": 1, "l2": 2}
+
+
+def _rope_inputs(q, k, q_weight, k_weight, cos_sin, positions, norm, eps, interleaved, first_position):
+    if norm not in _NORMS:
+        raise ValueError(f"norm must be 'rms', 'l2' or None, not {norm!r}")
+    B, T, Hq, d = q.shape
+    Hk = 0 if k is None else k.shape[2]
+    t = q.dtype
+    lds = []
+    for v, n, H in ((q, "q", Hq), (k, "k", Hk)):
+        if v is not None and v.numel() and (v.stride(-1) != 1 or (H > 1 and v.stride(-2) != d)):
+            raise ValueError(f"the heads of {n} must be dense and side by side")
+        lds.append(0 if v is None else _rows(v.flatten(-2) if v.numel() else v.reshape(B, T, H * d), n, (B, T), H * d,
+                                             t))
+    _check(q_weight, "q_weight", (d,), torch.float32)
+    _check(k_weight, "k_weight", (d,), torch.float32)
+    R = P = 0
+    if cos_sin is not None:
+        P, R = cos_sin.shape
+        _check(cos_sin, "cos_sin", (P, R), torch.float32)
+    _check(positions, "positions", (B, T), torch.int32)
+    return (B, T, Hq, Hk, d, _dt(q), _NORMS[norm], ctypes.c_float(eps), _some(q), lds[0], _some(k), lds[1],
+            _some(q_weight), _some(k_weight), R, int(bool(interleaved)), _some(cos_sin), P, _some(positions),
+            int(first_position))
+
+
+@_one_device
+def gdr2_head_norm_rope(q, k=None, q_weight=None, k_weight=None, cos_sin=None, positions=None, *, norm="rms",
+                        eps=1e-6, interleaved=False, first_position=0, q_out=None, k_out=None, stream=None):
+    """Norm of queries and keys per head and rotation by position, in one pass. Returns (q_out, k_out).
+
+    q: [B, T, Hq, d], k: [B, T, Hk, d] or None, views of a fused projection as they are (heads side by
+    side, d 64, 128 or 256); norm "rms" (x / sqrt(mean x^2 + eps)), "l2" (sum) or None; weights [d] fp32
+    or None. cos_sin [P, R] fp32 holds each position's R / 2 cosines and then sines (None: no rotation);
+    the first R channels turn in pairs (j, j + R / 2), or (2j, 2j + 1) if interleaved. positions [B, T]
+    int32, or None: token t is at first_position + t. A position outside the table leaves its token
+    unturned and the next gdr2_sync_status raises.
+    """
+    lib = load_library()
+    args = _rope_inputs(q, k, q_weight, k_weight, cos_sin, positions, norm, eps, interleaved, first_position)
+    qo = q_out if q_out is not None else torch.empty(tuple(q.shape), dtype=q.dtype, device=q.device)
+    _check(qo, "q_out", tuple(q.shape), q.dtype)
+    ko = None
+    if k is not None:
+        ko = k_out if k_out is not None else torch.empty(tuple(k.shape), dtype=q.dtype, device=q.device)
+        _check(ko, "k_out", tuple(k.shape), q.dtype)
+    _raise(lib, lib.gdr2_head_norm_rope(*args, _some(qo), _some(ko), _stream(stream)))
+    return qo, ko
+
+
+@_one_device
+def gdr2_head_norm_rope_backward(q, k, dq_out, dk_out=None, q_weight=None, k_weight=None, cos_sin=None, positions=None,
+                                 *, norm="rms", eps=1e-6, interleaved=False, first_position=0, workspace=None,
+                                 stream=None):
+    """Gradients of gdr2_head_norm_rope from its inputs and the outputs' gradients (contiguous).
+    Returns dict dq, dk, dq_weight, dk_weight (None for absent inputs)."""
+    lib = load_library()
+    args = _rope_inputs(q, k, q_weight, k_weight, cos_sin, positions, norm, eps, interleaved, first_position)
+    d, dev = q.shape[-1], q.device
+    _check(dq_out, "dq_out", tuple(q.shape), q.dtype)
+    if (k is None) != (dk_out is None):
+        raise ValueError("k and dk_out: both or neither")
+    if k is not None:
+        _check(dk_out, "dk_out", tuple(k.shape), q.dtype)
+    own = lambda t: None if t is None else torch.empty(tuple(t.shape), dtype=q.dtype, device=dev)  # noqa: E731
+    f32 = lambda w: None if w is None else torch.empty((d,), dtype=torch.float32, device=dev)  # noqa: E731
+    g = {"dq": own(q), "dk": own(k), "dq_weight": f32(q_weight), "dk_weight": f32(k_weight)}
+    workspace = _workspace(workspace, lib.gdr2_head_norm_rope_backward_workspace_bytes(d), dev)
+    st = lib.gdr2_head_norm_rope_backward(*args, _some(dq_out), _some(dk_out), _some(g["dq"]), _some(g["dk"]),
+                                          _some(g["dq_weight"]), _some(g["dk_weight"]), _some(workspace),
+                                          _nbytes(workspace), _stream(stream))
+    _raise(lib, st)
+    return g
 
 
 @_one_device

@@ -99,6 +99,82 @@ struct SegArgs {
     float *S_T;            // [B][H][dk][dv] or null: the state after the last segment
 };
 
+// Selective state-space scan (csrc/ssm_scan.cu, csrc/ssm_backward.cu).
+constexpr int kSsmChunk = 16;  // tokens between saved states
+
+struct SsmArgs {
+    int B, T, D, N;         // batch (sequences when packed), tokens, channels, states per channel
+    bool bf16, softplus;
+    const int *cu_seqlens;  // packed sequences (T = all tokens), or null (dense)
+    const void *x, *dt, *z, *Bm, *Cm;    // z may be null
+    long long ldx, lddt, ldz, ldb, ldc;  // elements from one token to the next
+    const float *A, *Dskip, *dt_bias, *S0;  // [D][N], [D] or null, [D] or null, [B][D][N] or null
+    void *y;                // null: the saved states alone (the backward's recomputation)
+    float *S_T;             // final states, or null; the step's resident state
+    float *saved_states;    // [B][ceil(T / kSsmChunk)][D][N], or null
+    void *workspace;
+};
+
+struct SsmGrads {
+    const void *dy;         // [B][T][D]
+    const float *dS_T;      // or null
+    void *dx, *ddt, *dz, *dBm, *dCm;  // dz null without z
+    float *dA, *dD, *dbias, *dS0;     // each may be null but dA
+};
+
+struct SsmSplit { int seg, nseg; };  // tokens per segment of the time axis, segments per stream
+SsmSplit ssm_split(int streams, int T, int D, int N);
+size_t ssm_scan_workspace_bytes(int streams, int T, int D, int N);
+cudaError_t launch_ssm_scan(const SsmArgs &a, cudaStream_t s);
+cudaError_t launch_ssm_step(const SsmArgs &a, cudaStream_t s);
+size_t ssm_backward_workspace_bytes(int B, int T, int D, int N, bool have_saved_states);
+cudaError_t launch_ssm_backward(const SsmArgs &a, const SsmGrads &g, cudaStream_t s);
+
+// Backward of the short convolution (csrc/conv_backward.cu), dense sequences.
+struct ConvBwdArgs {
+    int N, T, H, d, width;
+    bool bf16, l2norm;
+    float eps;
+    const void *x, *dy, *state_in, *dstate_out;  // states may be null
+    const float *weight;
+    void *dx, *dstate_in;                        // dstate_in may be null
+    float *dweight;
+    void *workspace;
+};
+size_t conv_backward_workspace_bytes(int N, int T, int H, int d);
+cudaError_t launch_conv_backward(const ConvBwdArgs &a, cudaStream_t s);
+
+// Per-head norm with rotation (csrc/head_norm_rope.cu).
+constexpr unsigned kStatusBadPosition = 4u;  // status word: a position outside the table
+
+struct HeadNormSide {
+    int H;                  // heads (0: this side is absent)
+    const void *x;          // [tokens] rows of H * d elements, ld apart
+    long long ld;
+    const float *weight;    // [d] or null
+    void *out;              // [tokens][H][d]; backward: dx
+    const void *dy;         // backward: [tokens][H][d]
+    float *dweight;         // backward: [d] or null
+};
+
+struct HeadNormArgs {
+    long long tokens;
+    int T;                  // tokens per sequence (positions null: token t of a sequence is at first + t)
+    int d, R, P;            // channels per head, rotated channels (0: none), rows of the table
+    int first;
+    bool bf16, interleaved;
+    int norm;               // 0 none, 1 rms, 2 l2
+    float eps;
+    const float *cos_sin;   // [P][R]: R / 2 cosines, then R / 2 sines
+    const int *positions;   // [tokens] or null
+    HeadNormSide side[2];   // queries, keys
+    void *workspace;        // backward's partial weight gradients
+    unsigned *status;
+};
+size_t head_norm_backward_workspace_bytes(int d);
+cudaError_t launch_head_norm_rope(const HeadNormArgs &a, cudaStream_t s);
+cudaError_t launch_head_norm_rope_backward(const HeadNormArgs &a, cudaStream_t s);
+
 cudaError_t launch_segment_states(const SegArgs &a, cudaStream_t s);
 
 // The backward's first two steps as one cooperative launch (fwd_tc.cu): the forward's chunk

@@ -1,0 +1,137 @@
+// seq_ops.h -- device helpers of the layers around the mixer (selective scan, convolution
+// backward, head norm): runs of consecutive elements held as raw words, and the
+// elementwise laws in fp32.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace gdr2 {
+namespace seq {
+
+// E consecutive elements of type T as 32-bit words (bf16 stays packed, two to a word).
+template <typename T, int E> struct Raw {
+    static constexpr int kWords = E * (int)sizeof(T) / 4;
+    static_assert(E * sizeof(T) % 4 == 0, "a run is whole words");
+    uint32_t w[kWords];
+
+    __device__ __forceinline__ void zero()
+    {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) w[i] = 0u;
+    }
+    __device__ __forceinline__ float get(int i) const
+    {
+        if constexpr (sizeof(T) == 2) return __uint_as_float((i & 1) ? (w[i / 2] & 0xffff0000u) : (w[i / 2] << 16));
+        else return __uint_as_float(w[i]);
+    }
+    // p: E elements, all valid and aligned to min(16, the run's bytes)
+    __device__ __forceinline__ void load_vec(const T *p)
+    {
+        if constexpr (kWords % 4 == 0) {
+#pragma unroll
+            for (int i = 0; i < kWords / 4; ++i) {
+                const uint4 a = __ldg(reinterpret_cast<const uint4 *>(p) + i);
+                w[4 * i] = a.x; w[4 * i + 1] = a.y; w[4 * i + 2] = a.z; w[4 * i + 3] = a.w;
+            }
+        } else if constexpr (kWords == 2) {
+            const uint2 a = __ldg(reinterpret_cast<const uint2 *>(p));
+            w[0] = a.x; w[1] = a.y;
+        } else {
+            static_assert(kWords == 1, "runs are 1, 2 or a multiple of 4 words");
+            w[0] = __ldg(reinterpret_cast<const uint32_t *>(p));
+        }
+    }
+    // the first `valid` elements one by one, zeros behind them
+    __device__ __forceinline__ void load_each(const T *p, int valid)
+    {
+        if constexpr (sizeof(T) == 2) {
+            const unsigned short *u = reinterpret_cast<const unsigned short *>(p);
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) {
+                const uint32_t lo = 2 * i < valid ? __ldg(u + 2 * i) : 0u;
+                const uint32_t hi = 2 * i + 1 < valid ? __ldg(u + 2 * i + 1) : 0u;
+                w[i] = lo | (hi << 16);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) w[i] = i < valid ? __ldg(reinterpret_cast<const uint32_t *>(p) + i) : 0u;
+        }
+    }
+};
+
+// bf16 pair, a in the low half
+__device__ __forceinline__ uint32_t pack2(float a, float b)
+{
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// E fp32 values to E elements of type T at p (rounded to nearest even)
+template <typename T, int E> __device__ __forceinline__ void store_vec(T *p, const float (&v)[E])
+{
+    constexpr int kWords = E * (int)sizeof(T) / 4;
+    uint32_t w[kWords];
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+        if constexpr (sizeof(T) == 2) w[i] = pack2(v[2 * i], v[2 * i + 1]);
+        else w[i] = __float_as_uint(v[i]);
+    }
+    if constexpr (kWords % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < kWords / 4; ++i)
+            reinterpret_cast<uint4 *>(p)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    } else if constexpr (kWords == 2) {
+        *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
+    } else {
+        static_assert(kWords == 1, "runs are 1, 2 or a multiple of 4 words");
+        *reinterpret_cast<uint32_t *>(p) = w[0];
+    }
+}
+template <typename T> __device__ __forceinline__ void store_one(T *p, float v)
+{
+    if constexpr (sizeof(T) == 2) *p = __float2bfloat16_rn(v);
+    else *p = v;
+}
+template <typename T, int E> __device__ __forceinline__ void store_each(T *p, const float (&v)[E], int valid)
+{
+#pragma unroll
+    for (int i = 0; i < E; ++i)
+        if (i < valid) store_one(p + i, v[i]);
+}
+template <typename T> __device__ __forceinline__ float load_one(const T *p)
+{
+    if constexpr (sizeof(T) == 2) return __bfloat162float(*p);
+    else return *p;
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// 2^x on the special-function unit (relative error 2^-22; 0 below the normal range)
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// log(1 + e^v), accurate for large negative v too (the small step sizes of a trained layer)
+__device__ __forceinline__ float softplus(float v) { return fmaxf(v, 0.f) + log1pf(expf(-fabsf(v))); }
+// 1 / (1 + e^-v); below v = -87 the denominator overflows and the quotient is 0
+__device__ __forceinline__ float sigmoid(float v) { return __fdividef(1.f, 1.f + expf(-v)); }
+
+// The sequence that token t of a packed stream belongs to: the last s in [0, N) with
+// cu[s] <= t (empty sequences share cu[s] with the next). Stays in [0, N) for any array.
+__device__ __forceinline__ int find_sequence(const int *cu, int N, int t)
+{
+    int lo = 0, hi = N - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (__ldg(cu + mid) <= t) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo;
+}
+
+}  // namespace seq
+}  // namespace gdr2

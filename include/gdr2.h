@@ -260,6 +260,24 @@ gdr2_status gdr2_short_conv_silu(int N, int T, int H, int d, gdr2_dtype dt, int 
                                  const void *state_in, void *state_out, void *y, void *stream);
 
 /*
+ * gdr2_short_conv_silu_backward -- gradients of gdr2_short_conv_silu over dense sequences:
+ *   of L = <y, dy> + <state_out, dstate_out> with respect to x, the taps and the state.
+ * in:  x, weight, state_in, width, l2norm, l2_eps as in the forward; dy [N, T, H, d] dt;
+ *      dstate_out [N][width - 1][H][d] dt or NULL (zero).
+ * out: dx [N, T, H, d] dt; dweight [H * d][width] fp32 (summed in fp32 in a fixed order);
+ *      dstate_in [N][width - 1][H][d] dt or NULL (not wanted).
+ * scratch: workspace of at least gdr2_short_conv_silu_backward_workspace_bytes(...) bytes,
+ *      16-byte aligned; its contents on entry do not matter.
+ * Output buffers must not overlap each other or an input. With N, H = 0 nothing is done; with
+ * T = 0 dweight is zero and dstate_in is dstate_out.
+ */
+size_t gdr2_short_conv_silu_backward_workspace_bytes(int N, int T, int H, int d, int width);
+gdr2_status gdr2_short_conv_silu_backward(int N, int T, int H, int d, gdr2_dtype dt, int width, int l2norm,
+                                          float l2_eps, const void *x, const float *weight, const void *state_in,
+                                          const void *dy, const void *dstate_out, void *dx, float *dweight,
+                                          void *dstate_in, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * gdr2_gate_activations -- the decay and gate branches' activations, element by element
  * over flat arrays (any layout: vector or scalar gates alike):
  *   log_alpha = -softplus(a) = -log(1 + e^a)   (so alpha = sigmoid(-a), in (0, 1))
@@ -270,6 +288,126 @@ gdr2_status gdr2_short_conv_silu(int N, int T, int H, int d, gdr2_dtype dt, int 
 gdr2_status gdr2_gate_activations(gdr2_dtype dt, long long n_alpha, const void *a, float *log_alpha,
                                   long long n_b, const void *b_pre, void *b,
                                   long long n_w, const void *w_pre, void *w, void *stream);
+
+/*
+ * Selective state-space scan: a diagonal mixer, with its own decay for each channel and state
+ * (the gated delta rule's decay is per key channel). Per channel c and state n, over the
+ * tokens of a sequence:
+ *
+ *   D_t[c] = softplus(step_t[c] + step_bias[c])   (softplus = 0: step_t[c] + step_bias[c])
+ *   h_t[c, n] = exp(D_t[c] A[c, n]) h_{t-1}[c, n] + D_t[c] Bm_t[n] x_t[c]
+ *   y_t[c] = (sum_n Cm_t[n] h_t[c, n] + Dskip[c] x_t[c]) * silu(z_t[c])
+ *
+ * Its input x is the short convolution's output (gdr2_short_conv_silu with l2norm = 0, its
+ * H * d channels taken as D), for prompts and for single tokens alike.
+ *
+ * Layouts: x, step, z are [B, T, D] in dt with `ld*` elements from one token to the next (views
+ *   of a fused projection; ld >= D, any element alignment: runs of 16 aligned bytes are read
+ *   where base, ld and D allow it, single elements otherwise); Bm, Cm are [B, T, N] in dt with their own ld >= N;
+ *   batch entries follow at T times ld. y is [B, T, D] dt, contiguous. A [D][N], Dskip [D],
+ *   step_bias [D] fp32; states [B][D][N] fp32. The pointers of A, the states, saved_states and the
+ *   workspace are 16-byte aligned, all others aligned to their element.
+ * Sizes: N is 8, 16, 32 or 64 (GDR2_ERR_UNSUPPORTED otherwise); B, T, D >= 0, any D. Arithmetic
+ *   and states are fp32; A may have either sign; nothing is clamped.
+ */
+#define GDR2_SSM_CHUNK 16 /* tokens between the saved states of gdr2_ssm_scan */
+
+/* Bytes of device scratch gdr2_ssm_scan needs (B = 1 stream when packed; 0 when the channels
+ * alone fill the GPU: the time axis is not cut then). Depends on the current device. */
+size_t gdr2_ssm_scan_workspace_bytes(int B, int T, int D, int N);
+
+/*
+ * gdr2_ssm_scan -- whole sequences, dense, or packed with cu_seqlens (as for
+ *   gdr2_forward_varlen: B sequences, T tokens in all, token tensors [T, .]).
+ * in:  Dskip, z, step_bias, S0 may be NULL (no skip, no gate, no bias, zero state).
+ * out: y; S_T [B][D][N] or NULL (a sequence without tokens keeps S0, or zeros);
+ *      saved_states [B][ceil(T / GDR2_SSM_CHUNK)][D][N] fp32 or NULL: the state before each chunk, for
+ *      gdr2_ssm_scan_backward (dense only).
+ * Output buffers must not overlap each other or an input (S_T may not be S0).
+ * cu_seqlens is not checked: an array that breaks the rule gives unspecified outputs, but every
+ * access stays inside the buffers above.
+ */
+gdr2_status gdr2_ssm_scan(int B, int T, int D, int N, gdr2_dtype dt, int softplus, const int *cu_seqlens,
+                          const void *x, long long ldx, const void *step, long long ldstep, const float *A,
+                          const void *Bm, long long ldb, const void *Cm, long long ldc, const float *Dskip,
+                          const void *z, long long ldz, const float *step_bias, const float *S0,
+                          void *y, float *S_T, float *saved_states,
+                          void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * gdr2_ssm_step -- one token for B resident states (decoding): x, step, z [B, D], Bm, Cm [B, N], y [B, D];
+ *   S [B][D][N] is read and written once, in place.
+ */
+gdr2_status gdr2_ssm_step(int B, int D, int N, gdr2_dtype dt, int softplus,
+                          const void *x, long long ldx, const void *step, long long ldstep, const float *A,
+                          const void *Bm, long long ldb, const void *Cm, long long ldc, const float *Dskip,
+                          const void *z, long long ldz, const float *step_bias, float *S, void *y, void *stream);
+
+/* Bytes of device scratch gdr2_ssm_scan_backward needs; more without saved states. */
+size_t gdr2_ssm_scan_backward_workspace_bytes(int B, int T, int D, int N, int have_saved_states);
+
+/*
+ * gdr2_ssm_scan_backward -- gradients of L = <y, dy> + <S_T, dS_T> of the dense scan, deterministic.
+ * in:  the forward's inputs; dy [B, T, D] dt, contiguous; dS_T [B][D][N] or NULL (zero);
+ *      saved_states as written by gdr2_ssm_scan for the same inputs, or NULL (formed again).
+ * out: dx, dstep, dz [B, T, D] dt (dz NULL without z); dBm, dCm [B, T, N] dt; all contiguous;
+ *      dA [D][N], dDskip [D], dstep_bias [D] fp32, dS0 [B][D][N] fp32; dDskip, dstep_bias and dS0 may be
+ *      NULL. dstep is the gradient of step before its bias and softplus.
+ * scratch: 256-byte aligned. Output buffers must not overlap each other or an input.
+ */
+gdr2_status gdr2_ssm_scan_backward(int B, int T, int D, int N, gdr2_dtype dt, int softplus,
+                                   const void *x, long long ldx, const void *step, long long ldstep, const float *A,
+                                   const void *Bm, long long ldb, const void *Cm, long long ldc, const float *Dskip,
+                                   const void *z, long long ldz, const float *step_bias, const float *S0,
+                                   const void *dy, const float *dS_T, const float *saved_states,
+                                   void *dx, void *dstep, float *dA, void *dBm, void *dCm, float *dDskip, void *dz,
+                                   float *dstep_bias, float *dS0,
+                                   void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * gdr2_head_norm_rope -- queries and keys of an attention layer (the sliding-window layers of
+ *   the notes' hybrid models): a norm over each head's d channels and the rotation by position,
+ *   in one pass over both.
+ *     xh = x / sqrt(mean x^2 + eps) (GDR2_NORM_RMS), x / sqrt(sum x^2 + eps) (GDR2_NORM_L2) or x
+ *     v = xh * weight;   y_a = v_a cos - v_b sin,  y_b = v_b cos + v_a sin
+ *   for the pairs (a, b) = (j, j + R / 2), or with interleaved (2 j, 2 j + 1), j < R / 2, of the first
+ *   R channels; the others are not turned.
+ * in:  q rows of Hq heads of d channels, ldq elements from one token to the next (a view of a
+ *      fused projection), k likewise with Hk, ldk (Hk = 0: no keys); tokens = B * T rows each;
+ *      q_weight, k_weight [d] fp32 or NULL (ones);
+ *      cos_sin [P][R] fp32: of each position R / 2 cosines, then R / 2 sines (NULL with R = 0);
+ *      positions [B * T] int32, DEVICE memory, or NULL: token t of every sequence is at
+ *      first_position + t. A position outside 0 .. P - 1 leaves its token unturned, and the next
+ *      gdr2_sync_status returns GDR2_ERR_INVALID_ARG.
+ * out: q_out [B * T][Hq][d], k_out [B * T][Hk][d], contiguous; they must not overlap an input.
+ * d is 64, 128 or 256; R a multiple of 16, at most d; eps finite and >= 0; q, k, the outputs and
+ * cos_sin are 16-byte aligned, ldq and ldk whole multiples of 16 bytes.
+ */
+#define GDR2_NORM_NONE 0
+#define GDR2_NORM_RMS 1
+#define GDR2_NORM_L2 2
+
+gdr2_status gdr2_head_norm_rope(int B, int T, int Hq, int Hk, int d, gdr2_dtype dt, int norm, float eps,
+                                const void *q, long long ldq, const void *k, long long ldk,
+                                const float *q_weight, const float *k_weight, int R, int interleaved,
+                                const float *cos_sin, int P, const int *positions, int first_position,
+                                void *q_out, void *k_out, void *stream);
+
+/* Bytes of device scratch gdr2_head_norm_rope_backward needs. */
+size_t gdr2_head_norm_rope_backward_workspace_bytes(int d);
+
+/*
+ * gdr2_head_norm_rope_backward -- its gradients: dq [B * T][Hq][d] and dk from q, k (the
+ *   forward's inputs) and dq_out, dk_out (contiguous, the outputs' layout); dq_weight, dk_weight [d] fp32 or
+ *   NULL (not wanted), summed in a fixed order. scratch: 16-byte aligned.
+ */
+gdr2_status gdr2_head_norm_rope_backward(int B, int T, int Hq, int Hk, int d, gdr2_dtype dt, int norm, float eps,
+                                         const void *q, long long ldq, const void *k, long long ldk,
+                                         const float *q_weight, const float *k_weight, int R, int interleaved,
+                                         const float *cos_sin, int P, const int *positions, int first_position,
+                                         const void *dq_out, const void *dk_out, void *dq, void *dk,
+                                         float *dq_weight, float *dk_weight,
+                                         void *workspace, size_t workspace_bytes, void *stream);
 
 /*
  * gdr2_segment_states -- the states entering the G segments of split sequences, for a
