@@ -42,6 +42,21 @@ template <typename T, int E> struct Raw {
             w[0] = __ldg(reinterpret_cast<const uint32_t *>(p));
         }
     }
+    // elements min(c + i, last) of a row, one by one: every load is in the row and none waits for a test
+    __device__ __forceinline__ void load_clamped(const T *row, int c, int last)
+    {
+        if constexpr (sizeof(T) == 2) {
+            const unsigned short *u = reinterpret_cast<const unsigned short *>(row);
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) {
+                const uint32_t lo = __ldg(u + min(c + 2 * i, last)), hi = __ldg(u + min(c + 2 * i + 1, last));
+                w[i] = lo | (hi << 16);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) w[i] = __ldg(reinterpret_cast<const uint32_t *>(row) + min(c + i, last));
+        }
+    }
     // the first `valid` elements one by one, zeros behind them
     __device__ __forceinline__ void load_each(const T *p, int valid)
     {
@@ -105,6 +120,17 @@ template <typename T> __device__ __forceinline__ float load_one(const T *p)
     else return *p;
 }
 
+// One element as raw bits, so that a load in flight is not waited for, and its value.
+template <typename T> __device__ __forceinline__ uint32_t load_bits(const T *p)
+{
+    if constexpr (sizeof(T) == 2) return __ldg(reinterpret_cast<const unsigned short *>(p));
+    else return __ldg(reinterpret_cast<const uint32_t *>(p));
+}
+template <typename T> __device__ __forceinline__ float bits_value(uint32_t b)
+{
+    return __uint_as_float(sizeof(T) == 2 ? b << 16 : b);
+}
+
 constexpr float kLog2e = 1.4426950408889634f;
 
 // 2^x on the special-function unit (relative error 2^-22; 0 below the normal range)
@@ -115,10 +141,75 @@ __device__ __forceinline__ float ex2(float x)
     return y;
 }
 
-// log(1 + e^v), accurate for large negative v too (the small step sizes of a trained layer)
-__device__ __forceinline__ float softplus(float v) { return fmaxf(v, 0.f) + log1pf(expf(-fabsf(v))); }
-// 1 / (1 + e^-v); below v = -87 the denominator overflows and the quotient is 0
-__device__ __forceinline__ float sigmoid(float v) { return __fdividef(1.f, 1.f + expf(-v)); }
+__device__ __forceinline__ float rcp(float x)  // 1 / x, one unit in the last place; 0 for infinity
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// log(1 + e^v) = max(v, 0) + log(1 + e), e = e^-|v| in (0, 1], with log(1 + e) = 2 atanh(s),
+// s = e / (2 + e) in (0, 1/3]: no cancellation for the small e of a trained layer's step
+// sizes, where log(1 + e) from the logarithm loses them. atanh(s) / s is a minimax polynomial
+// (Remez exchange) of degree 4 in s^2 on [0, 1/9], relative error 4e-9; in all 2e-7 (measured
+// by emulation; rms 6e-8). Two special-function instructions, against the library's
+// log1pf(expf()) about a third of the instructions.
+__device__ __forceinline__ float softplus(float v)
+{
+    const float e = ex2(-fabsf(v) * kLog2e);
+    const float s = e * rcp(2.f + e), t = s * s;
+    float p = fmaf(0.28178335f, t, 0.27960603f);
+    p = fmaf(p, t, 0.40024910f);
+    p = fmaf(p, t, 0.66666315f);
+    p = fmaf(p, t, 2.f);
+    return fmaf(s, p, fmaxf(v, 0.f));
+}
+// 1 / (1 + e^-v); below v = -88 the exponential overflows and the quotient is 0
+__device__ __forceinline__ float sigmoid(float v) { return rcp(1.f + ex2(-v * kLog2e)); }
+
+// Two fp32 values in one 64-bit register, and the instructions that work on both at once.
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pair(float lo, float hi)
+{
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void split(f32x2 v, float &lo, float &hi)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b)
+{
+    f32x2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b)
+{
+    f32x2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c)
+{
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f32x2 ex2x2(f32x2 v)
+{
+    float lo, hi;
+    split(v, lo, hi);
+    return pair(ex2(lo), ex2(hi));
+}
+// 16 bytes of shared memory as two pairs
+__device__ __forceinline__ void lds_pairs(const float *p, f32x2 &a, f32x2 &b)
+{
+    const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(p);
+    a = v.x;
+    b = v.y;
+}
 
 // The sequence that token t of a packed stream belongs to: the last s in [0, N) with
 // cu[s] <= t (empty sequences share cu[s] with the next). Stays in [0, N) for any array.

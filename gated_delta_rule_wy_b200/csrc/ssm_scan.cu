@@ -8,23 +8,30 @@
 // over whole sequences (dense or packed), and one token at a time on resident states.
 // All arithmetic is fp32.
 //
-// What bounds it: one exponential per (token, channel, state) -- 16 per 8 bytes of bf16
-// tokens moved at N = 16 -- so the scan is bound by the special-function and FMA pipes, not by
-// HBM; the single-token step reads and writes its state and is bound by HBM.
+// What bounds it: one exponential per (token, channel, state) on the special-function unit, 16 per
+// SM and cycle, and four for a (token, channel) (softplus and the gate): at N = 16 a floor of 172 us for 4 x 4096
+// tokens of 2048 channels, against 41 us of HBM traffic. The single-token step reads and
+// writes its state and is bound by HBM.
 //
-// Work split: N / 4 lanes per channel, four states in registers each (float4 loads of B and
-// C from shared memory, four independent chains), 256 threads walking a segment of the time
-// axis in tiles of 32 tokens. A tile's step sizes are formed once per (token, channel) by
-// the threads that load them, and the same threads finish y from the scan's sums, so x and
-// z stay in registers. Where the channels alone do not fill the GPU the time axis is cut in
-// segments: a first launch gives each segment's final state from zero and the sum of its
-// step sizes -- its transition is exp(A sum D), nothing else need be kept -- and the second
-// starts every segment from the composition of the ones before it.
+// Work split: a block owns 32 channels over a segment of the time axis, in tiles of 32 tokens. N / 4
+// scanning warps hold four states of each channel in registers, lane = channel: B and C are
+// broadcast reads of shared memory, no shuffles, and a token costs a warp 4 exponentials and about 17
+// other instructions. Four helper warps do what is done once per (token, channel): step sizes
+// ahead of the scan, and behind it the sum of the warps' parts, the skip and the gate. (Lanes of one
+// channel side by side, each token's work in the same threads, took 587 us; this form 248 us with
+// two blocks per SM, 69% of the floor; helpers alone 127 us, scanning warps alone 162 us.)
+//
+// Where the channels do not fill the GPU the time axis is cut in g segments: a first launch scans the
+// first segment whole and gives the others' final states from zero and the sums of their
+// step sizes -- a segment's transition is exp(A sum D), nothing else need be kept -- and the second
+// starts every later segment from the composition of the ones before it.
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
+
+#include <type_traits>
 
 #include "gdr2_launch.h"
 #include "seq_ops.h"
@@ -34,8 +41,12 @@ namespace {
 
 using namespace seq;
 
-constexpr int kThreads = 256;
-constexpr int kTile = 32;  // tokens per tile
+constexpr int kThreads = 256;   // of the single-token step
+constexpr int kCh = 32;         // channels per block: the lanes of a warp
+constexpr int kHelpers = 128;   // threads that convert tokens and finish outputs
+constexpr int kTile = 32;       // tokens per tile
+constexpr int E = kTile * kCh / kHelpers;  // consecutive channels a helper has of one token
+static_assert(kTile % kSsmChunk == 0 && E == 8, "a tile is whole chunks");
 
 struct ScanParams {
     int T, D, nseq;              // tokens per stream, channels, sequences
@@ -53,216 +64,308 @@ struct ScanParams {
     float *dsum;                 // [streams][nseg][D] sums of their step sizes
 };
 
-template <typename T, int N> struct ScanShape {
-    static constexpr int L = N / 4;            // lanes per channel
-    static constexpr int CH = kThreads / L;    // channels per block
-    static constexpr int E = CH / 8;           // consecutive channels a thread loads of one token
-    static constexpr int kPad = 8;             // y's four tokens of a step fall in different banks
-    static constexpr int kRow = CH + kPad;
+template <int N> struct ScanShape {
+    static constexpr int G = N / 4;                      // scanning warps
+    static constexpr int kBlock = 32 * G + kHelpers;
+    static constexpr int kStep = N == 64 ? 2 : 4;        // tokens whose shared-memory loads are in flight together
+    static constexpr int kBlocks = N <= 16 ? 2 : 1;      // per SM
+    // floats per token of (D, D x). The upper half's 16-byte chunks are swapped in pairs and rows are 8 floats
+    // apart from a multiple of 32: chunks written together fall in different banks
+    static constexpr int kDuRow = 2 * kCh + 8;
+    static constexpr int kYRow = kCh * G + 4;            // of the warps' parts of y
+    static constexpr int kDu = 0, kB = 2 * kTile * kDuRow, kC = kB + 2 * kTile * N, kY = kC + 2 * kTile * N;
+    static constexpr int kFloats = kY + 2 * kTile * kYRow;
+    static constexpr int kBC = N < 16 ? 1 : N / 16;      // runs of four elements of B (and C) per helper
 };
 
-// Sum over the L lanes of a channel of four tokens' partial sums; lanes 0 .. min(L, 4) - 1 end
-// up with the totals they write (L = 2: two tokens per lane).
-template <int L> __device__ __forceinline__ void reduce4(const float (&p)[4], int q, float (&out)[2], int &tok)
-{
-    const bool b0 = q & 1;
-    float k0 = b0 ? p[2] : p[0], k1 = b0 ? p[3] : p[1];
-    const float s0 = b0 ? p[0] : p[2], s1 = b0 ? p[1] : p[3];
-    k0 += __shfl_xor_sync(0xffffffffu, s0, 1);
-    k1 += __shfl_xor_sync(0xffffffffu, s1, 1);
-    tok = b0 ? 2 : 0;
-    if constexpr (L >= 4) {
-        const bool b1 = q & 2;
-        float k = b1 ? k1 : k0;
-        const float s = b1 ? k0 : k1;
-        k += __shfl_xor_sync(0xffffffffu, s, 2);
-        if constexpr (L >= 8) k += __shfl_xor_sync(0xffffffffu, k, 4);
-        if constexpr (L >= 16) k += __shfl_xor_sync(0xffffffffu, k, 8);
-        tok += b1 ? 1 : 0;
-        out[0] = k;
-    } else {
-        out[0] = k0;
-        out[1] = k1;
-    }
-}
-
+// One block: 32 channels over one segment of one stream. The first N / 4 warps scan tile i, lane = channel,
+// four states each; meanwhile the helpers turn tile i + 1 into (D, D x), finish the output of tile i - 1 and
+// have the loads of tile i + 2 in flight. One barrier per tile.
 template <typename T, int N, bool VEC, bool SUMMARY>
-__global__ void __launch_bounds__(kThreads) ssm_scan_kernel(ScanParams p)
+__device__ __forceinline__ void scan_segment(const ScanParams &p, int g, float *smem, unsigned (&smask)[2][2],
+                                             int (&sseq)[2][kTile])
 {
-    using S = ScanShape<T, N>;
-    constexpr int L = S::L, CH = S::CH, E = S::E, kRow = S::kRow;
-    constexpr int kBC = kTile * N / kThreads;  // elements of B (and of C) per thread
-    __shared__ __align__(16) float2 sdx[kTile * kRow];  // (D, D x); then y in .x
-    __shared__ __align__(16) float sB[kTile * N];
-    __shared__ __align__(16) float sC[SUMMARY ? 4 : kTile * N];
-    __shared__ unsigned smask[2];
-    __shared__ int sseq[kTile];
-
-    const int tid = threadIdx.x;
-    const int ncb = (p.D + CH - 1) / CH;
-    const int g = blockIdx.y, stream = blockIdx.x / ncb;
-    const int c0 = (blockIdx.x % ncb) * CH;
+    using S = ScanShape<N>;
+    constexpr int G = S::G, kBC = S::kBC, kStep = S::kStep;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int ncb = (p.D + kCh - 1) / kCh;
+    const int stream = blockIdx.x / ncb, c0 = blockIdx.x % ncb * kCh;
     const int tbeg = g * p.seg, tend = min(p.T, tbeg + p.seg);
-    // this thread's chain: channel c, states 4 q .. 4 q + 3
-    const int ch = tid / L, q = tid % L, c = c0 + ch;
-    const bool live = c < p.D;
-    // and the run of a tile it loads and finishes: token lr, channels c0 + lc .. + E - 1
-    const int lr = tid / 8, lc = (tid % 8) * E;
-    const int lvalid = min(E, p.D - (c0 + lc));
+    const int nt = (tend - tbeg + kTile - 1) / kTile;
 
-    float A2[4] = {0.f, 0.f, 0.f, 0.f}, h[4] = {0.f, 0.f, 0.f, 0.f};
-    if (live) {
-        const float4 a = *reinterpret_cast<const float4 *>(p.A + (size_t)c * N + 4 * q);
-        A2[0] = a.x * kLog2e; A2[1] = a.y * kLog2e; A2[2] = a.z * kLog2e; A2[3] = a.w * kLog2e;
-    }
-    auto load_state = [&](const float *base, size_t index, float (&v)[4]) {
-        const float4 a = *reinterpret_cast<const float4 *>(base + (index * p.D + c) * N + 4 * q);
-        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    };
-    auto store_state = [&](float *base, size_t index) {
-        *reinterpret_cast<float4 *>(base + (index * p.D + c) * N + 4 * q) = make_float4(h[0], h[1], h[2], h[3]);
-    };
-    auto initial = [&](int s) {  // the state before sequence s
-        if (p.S0 && live) load_state(p.S0, s, h);
-        else h[0] = h[1] = h[2] = h[3] = 0.f;
-    };
-    // the state entering this segment
-    if (!p.cu && g == 0) initial(stream);
-    if (!SUMMARY && g > 0 && live) {
-        int first = 0;  // the segment that holds the first token of the sequence at hand
-        if (p.cu) first = min(g, max(0, __ldg(p.cu + find_sequence(p.cu, p.nseq, tbeg))) / p.seg);
-        if (first < g) {
-            load_state(p.hloc, (size_t)stream * p.nseg + first, h);
-            for (int i = first + 1; i < g; ++i) {
-                const size_t at = (size_t)stream * p.nseg + i;
-                const float ds = p.dsum[at * p.D + c];
-                float o[4];
-                load_state(p.hloc, at, o);
+    if (warp < G) {  // ---------------------------------------------------------------- scan
+        const int c = c0 + lane, q = warp;
+        const bool live = c < p.D;
+        float A2[4] = {0.f, 0.f, 0.f, 0.f};
+        f32x2 h[2] = {0, 0};
+        if (live) {
+            const float4 a = *reinterpret_cast<const float4 *>(p.A + (size_t)c * N + 4 * q);
+            A2[0] = a.x * kLog2e; A2[1] = a.y * kLog2e; A2[2] = a.z * kLog2e; A2[3] = a.w * kLog2e;
+        }
+        auto load_state = [&](const float *base, size_t index, f32x2 (&v)[2]) {
+            const float4 a = *reinterpret_cast<const float4 *>(base + (index * p.D + c) * N + 4 * q);
+            v[0] = pair(a.x, a.y);
+            v[1] = pair(a.z, a.w);
+        };
+        auto store_state = [&](float *base, size_t index) {
+            float4 a;
+            split(h[0], a.x, a.y);
+            split(h[1], a.z, a.w);
+            *reinterpret_cast<float4 *>(base + (index * p.D + c) * N + 4 * q) = a;
+        };
+        auto decay = [&](float d, int k) { return pair(ex2(d * A2[2 * k]), ex2(d * A2[2 * k + 1])); };
+        auto initial = [&](int s) {  // the state before sequence s
+            if (p.S0 && live) load_state(p.S0, s, h);
+            else h[0] = h[1] = 0;
+        };
+        // the state entering this segment
+        if (!p.cu && g == 0) initial(stream);
+        if (!SUMMARY && g > 0 && live) {
+            int first = 0;  // the segment that holds the first token of the sequence at hand
+            if (p.cu) first = min(g, max(0, __ldg(p.cu + find_sequence(p.cu, p.nseq, tbeg))) / p.seg);
+            if (first < g) {
+                load_state(p.hloc, (size_t)stream * p.nseg + first, h);
+#pragma unroll 4
+                for (int i = first + 1; i < g; ++i) {
+                    const size_t at = (size_t)stream * p.nseg + i;
+                    const float ds = p.dsum[at * p.D + c];
+                    f32x2 o[2];
+                    load_state(p.hloc, at, o);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) h[k] = fmaf(ex2(ds * A2[k]), h[k], o[k]);
+                    for (int k = 0; k < 2; ++k) h[k] = fma2(decay(ds, k), h[k], o[k]);
+                }
             }
         }
+        struct Token {
+            float2 du;
+            f32x2 b[2], c[2];
+        };
+        const int chunk = lane / 2 ^ lane / 16;  // of this channel's (D, D x)
+        const float *sdu = smem + S::kDu + 4 * chunk + 2 * (lane & 1), *sB = smem + S::kB + 4 * q, *sC = smem + S::kC + 4 * q;
+        float *sy = smem + S::kY + kCh * q + lane;
+        float dsum = 0.f;
+        for (int it = 0; it < nt; ++it) {
+            __syncthreads();
+            const int buf = it & 1, t0 = tbeg + it * kTile;
+            auto load = [&](int t, Token &k) {
+                k.du = *reinterpret_cast<const float2 *>(sdu + (buf * kTile + t) * S::kDuRow);
+                lds_pairs(sB + (buf * kTile + t) * N, k.b[0], k.b[1]);
+                if constexpr (!SUMMARY) lds_pairs(sC + (buf * kTile + t) * N, k.c[0], k.c[1]);
+            };
+            unsigned mf = 0, ml = 0;
+            if (p.cu) { mf = smask[buf][0]; ml = smask[buf][1]; }
+            auto steps = [&](auto edges) {
+                constexpr bool EDGES = decltype(edges)::value;
+                Token now[kStep], next[kStep];
+#pragma unroll
+                for (int k = 0; k < kStep; ++k) load(k, now[k]);
+#pragma unroll
+                for (int st = 0; st < kTile; st += kStep) {
+                    if (st + kStep < kTile)
+#pragma unroll
+                        for (int k = 0; k < kStep; ++k) load(st + kStep + k, next[k]);
+                    if (!SUMMARY && st % kSsmChunk == 0 && p.saved && live && t0 + st < tend)
+                        store_state(p.saved, (size_t)stream * p.nchunk + (t0 + st) / kSsmChunk);
+#pragma unroll
+                    for (int k = 0; k < kStep; ++k) {
+                        const int t = st + k;
+                        if constexpr (EDGES)
+                            if ((mf >> t) & 1u) initial(sseq[buf][t]);
+                        const float d = now[k].du.x;
+                        const f32x2 u = pair(now[k].du.y, now[k].du.y);
+                        h[0] = fma2(decay(d, 0), h[0], mul2(u, now[k].b[0]));
+                        h[1] = fma2(decay(d, 1), h[1], mul2(u, now[k].b[1]));
+                        if constexpr (SUMMARY) {
+                            dsum += d;
+                        } else {
+                            float lo, hi;
+                            split(fma2(now[k].c[0], h[0], mul2(now[k].c[1], h[1])), lo, hi);
+                            sy[(buf * kTile + t) * S::kYRow] = lo + hi;
+                            if constexpr (EDGES)
+                                if (((ml >> t) & 1u) && p.S_T && live) store_state(p.S_T, sseq[buf][t]);
+                        }
+                    }
+#pragma unroll
+                    for (int k = 0; k < kStep; ++k) now[k] = next[k];
+                }
+            };
+            if ((mf | ml) != 0) steps(std::true_type{});
+            else steps(std::false_type{});
+        }
+        if constexpr (!SUMMARY) __syncthreads();
+        if (!live) return;
+        if (SUMMARY || (g == 0 && p.nseg > 2)) store_state(p.hloc, (size_t)stream * p.nseg + g);
+        if (SUMMARY && q == 0) p.dsum[((size_t)stream * p.nseg + g) * p.D + c] = dsum;
+        if (!SUMMARY && !p.cu && tend == p.T && p.S_T) store_state(p.S_T, stream);
+        return;
     }
+    // ---------------------------------------------------------------- helpers
+    const int hid = tid - 32 * G;
+    const int lr = hid / (kCh / E), lc = hid % (kCh / E) * E;  // its token of a tile, its first channel
+    const int lvalid = min(E, p.D - (c0 + lc));
     float bias[E], skip[E];
 #pragma unroll
     for (int i = 0; i < E; ++i) {
         bias[i] = p.bias && i < lvalid ? __ldg(p.bias + c0 + lc + i) : 0.f;
         skip[i] = !SUMMARY && p.Dskip && i < lvalid ? __ldg(p.Dskip + c0 + lc + i) : 0.f;
     }
-
     const T *x = static_cast<const T *>(p.x), *dt = static_cast<const T *>(p.dt), *z = static_cast<const T *>(p.z);
     const T *Bm = static_cast<const T *>(p.Bm), *Cm = static_cast<const T *>(p.Cm);
     T *y = static_cast<T *>(p.y);
+    // Loads are never conditional (a test before each would make them wait for one another): tokens past
+    // the segment and channels past D read the last one, and are made inert when converted.
+    const size_t row0 = (size_t)stream * p.T;
     auto load_run = [&](const T *base, long long ld, int t, Raw<T, E> &r) {
-        if (t >= tend || lvalid <= 0) { r.zero(); return; }
-        const T *src = base + ((size_t)stream * p.T + t) * ld + c0 + lc;
-        if constexpr (VEC) r.load_vec(src);
-        else r.load_each(src, lvalid);
+        const T *row = base + (row0 + min(t, tend - 1)) * ld;
+        if constexpr (VEC) r.load_vec(row + min(c0 + lc, p.D - E));
+        else r.load_clamped(row, c0 + lc, p.D - 1);
     };
-    Raw<T, E> rx, rdt, rz, nx, ndt, nz;
-    float nb[kBC], nc[kBC];
-    auto fetch = [&](int t0) {
-        load_run(x, p.ldx, t0 + lr, nx);
-        load_run(dt, p.lddt, t0 + lr, ndt);
-        if constexpr (!SUMMARY)
-            if (z) load_run(z, p.ldz, t0 + lr, nz);
+    struct Tokens {
+        Raw<T, E> x, dt;
+        uint32_t b[kBC][4], c[kBC][4];
+    };
+    constexpr int kRows = kHelpers / (N / 4);  // rows of B that the helpers read at once, four elements each
+    const int br = hid / (N / 4), bn = hid % (N / 4) * 4;
+    auto four = [](const uint32_t (&v)[4], bool in) {
+        return make_float4(in ? bits_value<T>(v[0]) : 0.f, in ? bits_value<T>(v[1]) : 0.f,
+                           in ? bits_value<T>(v[2]) : 0.f, in ? bits_value<T>(v[3]) : 0.f);
+    };
+    auto fetch = [&](int t0, Tokens &k) {
+        load_run(x, p.ldx, t0 + lr, k.x);
+        load_run(dt, p.lddt, t0 + lr, k.dt);
 #pragma unroll
         for (int i = 0; i < kBC; ++i) {
-            const int r = (tid + i * kThreads) / N, n = (tid + i * kThreads) % N, t = t0 + r;
-            const size_t row = (size_t)stream * p.T + t;
-            nb[i] = t < tend ? load_one(Bm + row * p.ldb + n) : 0.f;
-            if constexpr (!SUMMARY) nc[i] = t < tend ? load_one(Cm + row * p.ldc + n) : 0.f;
+            const size_t row = row0 + min(t0 + br + i * kRows, tend - 1);
+            const T *b = Bm + row * p.ldb + bn, *c = Cm + row * p.ldc + bn;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                k.b[i][j] = load_bits(b + j);
+                if constexpr (!SUMMARY) k.c[i][j] = load_bits(c + j);
+            }
         }
     };
-    float dsum = 0.f;
-    fetch(tbeg);
-    for (int t0 = tbeg; t0 < tend; t0 += kTile) {
-        rx = nx; rdt = ndt; rz = nz;
-        // step sizes of this thread's run; tokens past the segment and channels past D are inert (D = 0)
-        const bool run_ok = t0 + lr < tend;
+    // the fetched tile into buffer `buf`; tokens past the segment and channels past D are inert
+    // (D = 0: the decay is 1 and nothing is added)
+    auto convert = [&](const Tokens &tok, int t0, int buf) {
+        float4 *dst = reinterpret_cast<float4 *>(smem + S::kDu + (buf * kTile + lr) * S::kDuRow + 2 * lc);
+        const int swap = lc / (kCh / 2);
+        const bool in = t0 + lr < tend;
+        float d[E];
 #pragma unroll
-        for (int i = 0; i < E; ++i) {
-            const float v = rdt.get(i) + bias[i];
-            const float d = run_ok && i < lvalid ? (p.softplus ? softplus(v) : v) : 0.f;
-            sdx[lr * kRow + lc + i] = make_float2(d, d * rx.get(i));
-        }
+        for (int i = 0; i < E; ++i) d[i] = tok.dt.get(i) + bias[i];
+        if (p.softplus)
+#pragma unroll
+            for (int i = 0; i < E; ++i) d[i] = softplus(d[i]);
+        float u[E];
+#pragma unroll
+        for (int i = 0; i < E; ++i) u[i] = d[i] * tok.x.get(i);
+        if (t0 + kTile > tend || lvalid < E)
+#pragma unroll
+            for (int i = 0; i < E; ++i)
+                if (!in || i >= lvalid) d[i] = u[i] = 0.f;
+#pragma unroll
+        for (int i = 0; i < E; i += 2)
+            dst[i / 2 + (i % 4 == 0 ? swap : -swap)] = make_float4(d[i], u[i], d[i + 1], u[i + 1]);
 #pragma unroll
         for (int i = 0; i < kBC; ++i) {
-            sB[tid + i * kThreads] = nb[i];
-            if constexpr (!SUMMARY) sC[tid + i * kThreads] = nc[i];
+            const int r = br + i * kRows, at = (buf * kTile + r) * N + bn;
+            if (r < kTile) {
+                *reinterpret_cast<float4 *>(smem + S::kB + at) = four(tok.b[i], t0 + r < tend);
+                if constexpr (!SUMMARY) *reinterpret_cast<float4 *>(smem + S::kC + at) = four(tok.c[i], t0 + r < tend);
+            }
         }
-        if (p.cu && tid < 32) {
-            const int t = t0 + tid;
+        if (p.cu && hid < 32) {  // packed: which of the tile's tokens begin and end a sequence
+            const int t = t0 + hid;
             bool first = false, last = false;
             if (t < tend) {
                 const int s = find_sequence(p.cu, p.nseq, t);
-                sseq[tid] = s;
+                sseq[buf][hid] = s;
                 first = __ldg(p.cu + s) == t;
                 last = __ldg(p.cu + s + 1) == t + 1;
             }
             const unsigned mf = __ballot_sync(0xffffffffu, first), ml = __ballot_sync(0xffffffffu, last);
-            if (tid == 0) { smask[0] = mf; smask[1] = ml; }
+            if (hid == 0) { smask[buf][0] = mf; smask[buf][1] = ml; }
         }
-        __syncthreads();
-        if (t0 + kTile < tend) fetch(t0 + kTile);
-        unsigned mf = 0, ml = 0;
-        if (p.cu) { mf = smask[0]; ml = smask[1]; }
-        const bool edges = (mf | ml) != 0;
-#pragma unroll 2
-        for (int tt = 0; tt < kTile; tt += 4) {
-            if (!SUMMARY && p.saved && tt % kSsmChunk == 0 && t0 + tt < tend && live)
-                store_state(p.saved, (size_t)stream * p.nchunk + (t0 + tt) / kSsmChunk);
-            float part[4];
+    };
+    struct Outer {
+        Raw<T, E> x, z;
+    };
+    auto fetch_outer = [&](int t0, Outer &k) {
+        if (SUMMARY || !y) return;
+        load_run(x, p.ldx, t0 + lr, k.x);
+        if (z) load_run(z, p.ldz, t0 + lr, k.z);
+    };
+    auto finish = [&](const Outer &k, int t0, int buf) {
+        if (t0 + lr >= tend || lvalid <= 0 || !y) return;
+        float o[E];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int t = tt + k;
-                if (edges && ((mf >> t) & 1u)) initial(sseq[t]);
-                const float2 dx = sdx[t * kRow + ch];
-                const float4 b = *reinterpret_cast<const float4 *>(sB + t * N + 4 * q);
-                h[0] = fmaf(ex2(dx.x * A2[0]), h[0], dx.y * b.x);
-                h[1] = fmaf(ex2(dx.x * A2[1]), h[1], dx.y * b.y);
-                h[2] = fmaf(ex2(dx.x * A2[2]), h[2], dx.y * b.z);
-                h[3] = fmaf(ex2(dx.x * A2[3]), h[3], dx.y * b.w);
-                if constexpr (SUMMARY) {
-                    dsum += dx.x;
-                } else {
-                    const float4 cv = *reinterpret_cast<const float4 *>(sC + t * N + 4 * q);
-                    part[k] = fmaf(cv.x, h[0], cv.y * h[1]) + fmaf(cv.z, h[2], cv.w * h[3]);
-                    if (edges && ((ml >> t) & 1u) && p.S_T && live) store_state(p.S_T, sseq[t]);
-                }
-            }
-            if constexpr (!SUMMARY) {
-                float out[2];
-                int tok;
-                reduce4<L>(part, q, out, tok);  // every lane has read its step's (D, D x) before
-                if (q < 4) {
-                    sdx[(tt + tok) * kRow + ch].x = out[0];
-                    if constexpr (L == 2) sdx[(tt + tok + 1) * kRow + ch].x = out[1];
-                }
-            }
-        }
-        __syncthreads();
-        if constexpr (!SUMMARY) {
-            if (run_ok && lvalid > 0 && y) {
-                float o[E];
+        for (int i = 0; i < E; ++i) o[i] = skip[i] * k.x.get(i);
+        const float *src = smem + S::kY + (buf * kTile + lr) * S::kYRow + lc;
 #pragma unroll
-                for (int i = 0; i < E; ++i) {
-                    o[i] = fmaf(skip[i], rx.get(i), sdx[lr * kRow + lc + i].x);
-                    if (z) { const float zv = rz.get(i); o[i] *= zv * sigmoid(zv); }
-                }
-                T *dst = y + ((size_t)stream * p.T + t0 + lr) * p.D + c0 + lc;
-                if constexpr (VEC) store_vec<T, E>(dst, o);
-                else store_each<T, E>(dst, o, lvalid);
+        for (int w = 0; w < G; ++w)
+#pragma unroll
+            for (int i = 0; i < E; i += 4) {
+                const float4 v = *reinterpret_cast<const float4 *>(src + w * kCh + i);
+                o[i] += v.x; o[i + 1] += v.y; o[i + 2] += v.z; o[i + 3] += v.w;
             }
-        }
+        if (z)
+#pragma unroll
+            for (int i = 0; i < E; ++i) { const float zv = k.z.get(i); o[i] *= zv * sigmoid(zv); }
+        T *dst = y + ((size_t)stream * p.T + t0 + lr) * p.D + c0 + lc;
+        if constexpr (VEC) store_vec<T, E>(dst, o);
+        else store_each<T, E>(dst, o, lvalid);
+    };
+    // Each of the four helpers of a token asks for one tensor's row, kAhead tiles before it is loaded: loads
+    // then come from L2 and return before the next tile (from HBM they take longer than a tile's work).
+    constexpr int kAhead = 3;
+    const T *const pbase[4] = {x + c0, dt + c0, z ? z + c0 : x + c0, SUMMARY || hid % 8 < 4 ? Bm : Cm};
+    const long long pld[4] = {p.ldx, p.lddt, z ? p.ldz : p.ldx, SUMMARY || hid % 8 < 4 ? p.ldb : p.ldc};
+    const T *prow = pbase[0];
+    long long prl = pld[0];
+#pragma unroll
+    for (int i = 1; i < 4; ++i)
+        if (hid % 4 == i) { prow = pbase[i]; prl = pld[i]; }
+    auto prefetch = [&](int t0) {
+        const T *row = prow + (row0 + min(t0 + lr, tend - 1)) * prl;
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(row));
+    };
+    Tokens tok;
+    Outer out;
+    if (nt > 0) {
+#pragma unroll
+        for (int k = 1; k <= kAhead; ++k) prefetch(tbeg + k * kTile);
+        fetch(tbeg, tok);
+        convert(tok, tbeg, 0);
+        fetch(tbeg + kTile, tok);
     }
-    if (!live) return;
-    if constexpr (SUMMARY) {
-        const size_t at = (size_t)stream * p.nseg + g;
-        store_state(p.hloc, at);
-        if (q == 0) p.dsum[at * p.D + c] = dsum;
-    } else if (!p.cu && tend == p.T && p.S_T) {
-        store_state(p.S_T, stream);
+    for (int it = 0; it < nt; ++it) {
+        __syncthreads();
+        const int t0 = tbeg + it * kTile;
+        convert(tok, t0 + kTile, (it + 1) & 1);
+        if (!SUMMARY && it > 0) finish(out, t0 - kTile, (it - 1) & 1);
+        fetch(t0 + 2 * kTile, tok);
+        fetch_outer(t0, out);
+        prefetch(t0 + (2 + kAhead) * kTile);
+    }
+    if constexpr (!SUMMARY) {
+        __syncthreads();
+        if (nt > 0) finish(out, tbeg + (nt - 1) * kTile, (nt - 1) & 1);
+    }
+}
+
+// FIRST (three segments or more): the first segment whole and the others' summaries, up to the last
+// but one; otherwise all segments (one), or those from the second on.
+template <typename T, int N, bool VEC, bool FIRST>
+__global__ void __launch_bounds__(ScanShape<N>::kBlock, ScanShape<N>::kBlocks) ssm_scan_kernel(ScanParams p)
+{
+    extern __shared__ __align__(16) float smem[];
+    __shared__ unsigned smask[2][2];
+    __shared__ int sseq[2][kTile];
+    if constexpr (FIRST) {
+        if (blockIdx.y == 0) scan_segment<T, N, VEC, false>(p, 0, smem, smask, sseq);
+        else scan_segment<T, N, VEC, true>(p, blockIdx.y, smem, smask, sseq);
+    } else {
+        scan_segment<T, N, VEC, false>(p, p.nseg > 1 ? blockIdx.y + 1 : 0, smem, smask, sseq);
     }
 }
 
@@ -356,24 +459,25 @@ bool runs_aligned(const void *p, long long ld, int esz, int bytes)
 template <typename T, int N>
 cudaError_t launch_scan(const SsmArgs &a, const ScanParams &p, cudaStream_t st)
 {
-    using S = ScanShape<T, N>;
+    using S = ScanShape<N>;
     const int streams = a.cu_seqlens ? 1 : a.B;
-    const unsigned cb = (unsigned)((a.D + S::CH - 1) / S::CH);
-    const int bytes = S::E * (int)sizeof(T) < 16 ? S::E * (int)sizeof(T) : 16;
-    const bool vec = a.D % S::E == 0 && runs_aligned(a.x, a.ldx, sizeof(T), bytes) &&
-                     runs_aligned(a.dt, a.lddt, sizeof(T), bytes) && runs_aligned(a.z, a.ldz, sizeof(T), bytes) &&
-                     runs_aligned(a.y, a.D, sizeof(T), bytes);
+    const unsigned cb = (unsigned)((a.D + kCh - 1) / kCh);
+    auto ok = [&](const void *q, long long ld) { return runs_aligned(q, ld, sizeof(T), 16); };
+    const bool vec = a.D % E == 0 && ok(a.x, a.ldx) && ok(a.dt, a.lddt) && ok(a.z, a.ldz) && ok(a.y, a.D);
+    auto run = [&](auto *kern, int segments) -> cudaError_t {
+        const int smem = S::kFloats * (int)sizeof(float);
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        kern<<<dim3(cb * streams, segments), S::kBlock, smem, st>>>(p);
+        return cudaGetLastError();
+    };
     if (p.nseg > 1) {
-        const dim3 grid(cb * streams, p.nseg - 1);
-        if (vec) ssm_scan_kernel<T, N, true, true><<<grid, kThreads, 0, st>>>(p);
-        else ssm_scan_kernel<T, N, false, true><<<grid, kThreads, 0, st>>>(p);
-        const cudaError_t e = cudaGetLastError();
+        const cudaError_t e = vec ? run(ssm_scan_kernel<T, N, true, true>, p.nseg - 1)
+                                  : run(ssm_scan_kernel<T, N, false, true>, p.nseg - 1);
         if (e != cudaSuccess) return e;
     }
-    const dim3 grid(cb * streams, p.nseg);
-    if (vec) ssm_scan_kernel<T, N, true, false><<<grid, kThreads, 0, st>>>(p);
-    else ssm_scan_kernel<T, N, false, false><<<grid, kThreads, 0, st>>>(p);
-    return cudaGetLastError();
+    const int rest = p.nseg > 1 ? p.nseg - 1 : 1;
+    return vec ? run(ssm_scan_kernel<T, N, true, false>, rest) : run(ssm_scan_kernel<T, N, false, false>, rest);
 }
 
 template <typename T>
@@ -404,7 +508,32 @@ cudaError_t launch_step_n(const SsmArgs &a, const StepParams &p, cudaStream_t st
 
 }  // namespace
 
-// Segments of the time axis: enough blocks to fill the GPU four times over, segments of at
+// Segments of the time axis. With one the scan is a single launch of a block per 32 channels; with
+// g > 2 two launches of g - 1 blocks per 32 channels, each over T / g tokens. A token costs an SM that runs k blocks,
+// two at a time, k units, and a block that is alone kAlone (at N = 16: 30 ns a unit, 38 ns alone).
+SsmSplit ssm_scan_split(int streams, int T, int D, int N)
+{
+    constexpr double kAlone = 1.27;
+    const long long blocks = (long long)streams * ((D + kCh - 1) / kCh);
+    const int sms = sm_count(), tiles = (T + kTile - 1) / kTile;
+    auto cost = [&](int g) {
+        const long long k = (blocks * (g > 1 ? g - 1 : 1) + sms - 1) / sms;
+        const double per = ((tiles + g - 1) / g * (double)kTile + 64.) * (k % 2 ? k - 1 + kAlone : k);
+        return g > 1 ? 2 * per + 2. * g : per;  // with a tile to fill and a tile to drain; states to compose
+    };
+    int best = 1;
+    for (int g = 3; g <= tiles && g <= 256; ++g)
+        if (cost(g) < cost(best)) best = g;
+    SsmSplit s;
+    s.seg = (tiles + best - 1) / best * kTile;
+    if (s.seg < kTile) s.seg = kTile;
+    s.nseg = (T + s.seg - 1) / s.seg;
+    if (s.nseg == 2) { s.nseg = 1; s.seg = (tiles > 0 ? tiles : 1) * kTile; }
+    if (s.nseg < 1) s.nseg = 1;
+    return s;
+}
+
+// Segments of the backward: enough blocks to fill the GPU four times over, segments of at
 // least 64 tokens, and none where the channels alone give two blocks per SM.
 SsmSplit ssm_split(int streams, int T, int D, int N)
 {
@@ -415,8 +544,8 @@ SsmSplit ssm_split(int streams, int T, int D, int N)
     if (g > most) g = most;
     if (g < 1) g = 1;
     SsmSplit s;
-    s.seg = (int)(((T + g - 1) / g + kTile - 1) / kTile * kTile);
-    if (s.seg < kTile) s.seg = kTile;
+    s.seg = (int)(((T + g - 1) / g + kSsmChunk - 1) / kSsmChunk * kSsmChunk);
+    if (s.seg < kSsmChunk) s.seg = kSsmChunk;
     s.nseg = (T + s.seg - 1) / s.seg;
     if (s.nseg < 1) s.nseg = 1;
     return s;
@@ -424,7 +553,7 @@ SsmSplit ssm_split(int streams, int T, int D, int N)
 
 size_t ssm_scan_workspace_bytes(int streams, int T, int D, int N)
 {
-    const SsmSplit s = ssm_split(streams, T, D, N);
+    const SsmSplit s = ssm_scan_split(streams, T, D, N);
     if (s.nseg <= 1) return 0;
     const size_t n = (size_t)streams * s.nseg * D;
     return (n * (N + 1) * sizeof(float) + 255) / 256 * 256;
@@ -434,7 +563,7 @@ cudaError_t launch_ssm_scan(const SsmArgs &a, cudaStream_t st)
 {
     const int streams = a.cu_seqlens ? 1 : a.B;
     if (a.T > 0 && streams > 0 && a.D > 0) {
-        const SsmSplit s = ssm_split(streams, a.T, a.D, a.N);
+        const SsmSplit s = ssm_scan_split(streams, a.T, a.D, a.N);
         ScanParams p;
         p.T = a.T; p.D = a.D; p.nseq = a.B;
         p.seg = s.seg; p.nseg = s.nseg;
