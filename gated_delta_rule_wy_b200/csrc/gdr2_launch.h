@@ -123,8 +123,6 @@ struct SsmGrads {
 };
 
 struct SsmSplit { int seg, nseg; };  // tokens per segment of the time axis, segments per stream
-SsmSplit ssm_scan_split(int streams, int T, int D, int N);
-SsmSplit ssm_split(int streams, int T, int D, int N);
 size_t ssm_scan_workspace_bytes(int streams, int T, int D, int N);
 cudaError_t launch_ssm_scan(const SsmArgs &a, cudaStream_t s);
 cudaError_t launch_ssm_step(const SsmArgs &a, cudaStream_t s);

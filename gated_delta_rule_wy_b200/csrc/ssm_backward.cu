@@ -9,20 +9,27 @@
 //   dA = sum_t D_t m_t,  dDskip = sum g x,  dbias = sum ddt,  dS0 = a_0 dh_0
 //   dz_t = dy_t y'_t silu'(z_t) with y' the output before its gate, formed again here.
 //
-// The states are formed again from the ones saved every kSsmChunk tokens: per chunk a thread
-// runs its four states forward and keeps them in registers (64 of them), then walks back.
-// The two sums over channels (dB, dC) are taken over a warp's channels by shuffles that halve
-// the values with each step, over a block's warps in shared memory and over the blocks by a
-// last kernel, in a fixed order: no atomics, the same bits each time.
+// Work split as in the forward: a block owns 32 channels over a segment of the time axis, in tiles
+// of kSsmChunk tokens from the last to the first. Scanning warps (lane = channel, four states each) form a
+// tile's states again from the one saved before it, eight tokens at a time in registers (the first eight
+// twice: 32 registers instead of 64 let two blocks share an SM), and walk back; helper warps form the step sizes and gates of the tile to the left and the token gradients of the
+// tile to the right meanwhile.
 //
-// Segments of the time axis as in the forward: each segment's own part of the gradient that
-// leaves it to the left and the sum of its step sizes, then every segment from the
-// composition of those to its right.
+// The sums over channels (dB, dC) are taken over a warp's 32 lanes by shuffles that halve the values with each step.
+// Lane l holds its four states in the order j ^ (l & 3): in the first two steps every lane then keeps its low
+// half and gives its high half, without selects (shared memory has B and C in the four orders). The blocks' sums
+// are added by a last kernel in a fixed order: no atomics, the same bits each time.
+//
+// Segments of the time axis as in the forward, from the right: the first launch walks the last segment
+// whole and gives the others' own part of the gradient that leaves them to the left and the sums of their
+// step sizes; the second starts each of the others from the composition of those to its right.
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
+
+#include <type_traits>
 
 #include "gdr2_launch.h"
 #include "seq_ops.h"
@@ -32,8 +39,12 @@ namespace {
 
 using namespace seq;
 
-constexpr int kThreads = 256;
+constexpr int kCh = 32;         // channels per block: the lanes of a warp
 constexpr int kTile = kSsmChunk;
+constexpr int kHalf = kTile / 2;  // tokens whose states are in registers at a time
+constexpr int kHelpers = 128;
+constexpr int E = kTile * kCh / kHelpers;  // consecutive channels a helper has of one token
+static_assert(E == 4, "a helper has four channels");
 
 struct BwdParams {
     int B, T, D, seg, nseg, nchunk, ncb;
@@ -50,291 +61,452 @@ struct BwdParams {
 };
 
 template <int N> struct BwdShape {
-    static constexpr int L = N / 4;
-    static constexpr int CH = kThreads / L;
-    static constexpr int E = CH / 16 < 2 ? 2 : CH / 16;  // channels a thread loads of one token
-    static constexpr int kPerRow = CH / E;               // threads per token (16; 8 at N = 64)
-    static constexpr int kPad = 8;
-    static constexpr int kRow = CH + kPad;
-    static constexpr int kWarps = kThreads / 32;
-    // shared memory, in floats: (D, D x) then (du, sum A m); g; y before its gate; B; C; the warps' sums
-    static constexpr int kDx = 0, kG = 2 * kTile * kRow, kY = kG + kTile * kRow, kB = kY + kTile * kRow;
-    static constexpr int kC = kB + kTile * N, kRed = kC + kTile * N, kFloats = kRed + kWarps * kTile * 2 * N;
+    static constexpr int G = N < 32 ? N / 4 : 8;    // scanning warps
+    static constexpr int R = N / (4 * G);           // sets of four states a warp walks one after the other
+    static constexpr int kBlock = 32 * G + kHelpers;
+    static constexpr int kBlocks = N <= 16 ? 2 : 1; // per SM
+    static constexpr int kDuRow = 2 * kCh + 8, kGRow = kCh + 4, kPRow = kCh * G + 4;
+    static constexpr int kBCRow = 8 * N;            // of one token: B and C, of every four states the four orders
+    // shared memory, in floats: (D, D x); g; B and C; the warps' parts of du, dD and y; the sums over channels;
+    // what a helper keeps of its elements from their conversion to their gradients
+    static constexpr int kDu = 0, kG = kDu + 2 * kTile * kDuRow, kBC = kG + 2 * kTile * kGRow;
+    static constexpr int kPart = kBC + 2 * kTile * kBCRow, kSum = kPart + 2 * 3 * kTile * kPRow;
+    static constexpr int kKeep = kSum + 2 * kTile * 2 * N;
+    static constexpr int kFloats = kKeep + 3 * 5 * 4 * kHelpers;
+    static constexpr int kRuns = N < 16 ? 1 : N / 16;  // runs of four elements of B and C per helper
 };
 
-// Sum over a warp's 32 / L channels (lane bits log2 L .. 4) of eight values per lane, which
-// halve with each step; lane (channel bits j) ends with value(s) index0 ...; returns how many.
-template <int L> struct ChannelSum {
-    static constexpr int kLeft = L == 2 ? 1 : L == 4 ? 1 : L == 8 ? 2 : 4;  // values per lane at the end
-    __device__ __forceinline__ static void run(float (&v)[8], int lane, int &index)
-    {
-        index = 0;
-        int width = 8;
-#pragma unroll
-        for (int m = L; m < 32; m <<= 1) {
-            if (width > 1) {
-                const bool up = lane & m;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if (i < width / 2) {
-                        const float keep = up ? v[i + width / 2] : v[i];
-                        const float give = up ? v[i] : v[i + width / 2];
-                        v[i] = keep + __shfl_xor_sync(0xffffffffu, give, m);
-                    }
-                }
-                width /= 2;
-                index += up ? width : 0;
-            } else {
-                v[0] += __shfl_xor_sync(0xffffffffu, v[0], m);
-            }
-        }
-    }
-};
-
-template <int L> __device__ __forceinline__ float lane_sum(float v)
+// v[j] <-> v[j ^ order]: from the natural order of four states to a lane's and back
+__device__ __forceinline__ void reorder(float (&v)[4], int order)
 {
-#pragma unroll
-    for (int m = 1; m < L; m <<= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
-    return v;
+    const bool hi = order & 2, lo = order & 1;
+    const float a = hi ? v[2] : v[0], b = hi ? v[3] : v[1], c = hi ? v[0] : v[2], d = hi ? v[1] : v[3];
+    v[0] = lo ? b : a; v[1] = lo ? a : b; v[2] = lo ? d : c; v[3] = lo ? c : d;
+}
+
+// Sums over the 32 lanes of b and c, four states in the lane's order: lane l, and every 8th from it,
+// returns the sum of state l & 3, of b where l & 4 is 0 and of c where not.
+__device__ __forceinline__ float channel_sum(const float (&b)[4], const float (&c)[4], int lane)
+{
+    constexpr unsigned all = 0xffffffffu;
+    const float b0 = b[0] + __shfl_xor_sync(all, b[2], 2), b1 = b[1] + __shfl_xor_sync(all, b[3], 2);
+    const float c0 = c[0] + __shfl_xor_sync(all, c[2], 2), c1 = c[1] + __shfl_xor_sync(all, c[3], 2);
+    const float bs = b0 + __shfl_xor_sync(all, b1, 1), cs = c0 + __shfl_xor_sync(all, c1, 1);
+    const bool up = lane & 4;
+    float v = (up ? cs : bs) + __shfl_xor_sync(all, up ? bs : cs, 4);
+    v += __shfl_xor_sync(all, v, 8);
+    return v + __shfl_xor_sync(all, v, 16);
 }
 
 // SUMMARY: the segment's own part of the gradient that leaves it to the left, and sum D.
 template <typename T, int N, bool VEC, bool SUMMARY>
-__global__ void __launch_bounds__(kThreads) ssm_backward_kernel(BwdParams p)
+__device__ __forceinline__ void walk_segment(const BwdParams &p, int g, float *smem)
 {
     using S = BwdShape<N>;
-    constexpr int L = S::L, CH = S::CH, E = S::E, kRow = S::kRow;
-    constexpr int kBC = (kTile * N + kThreads - 1) / kThreads;
-    extern __shared__ __align__(16) float smem[];
-    float2 *sdx = reinterpret_cast<float2 *>(smem + S::kDx);
-    float *sg = smem + S::kG, *sy = smem + S::kY, *sB = smem + S::kB, *sC = smem + S::kC, *sred = smem + S::kRed;
-
+    constexpr int G = S::G, R = S::R;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int stream = blockIdx.x / p.ncb, cb = blockIdx.x % p.ncb;
-    const int g = SUMMARY ? blockIdx.y + 1 : blockIdx.y;
-    const int c0 = cb * CH;
+    const int stream = blockIdx.x / p.ncb, cb = blockIdx.x % p.ncb, c0 = cb * kCh;
     const int tbeg = g * p.seg, tend = min(p.T, tbeg + p.seg);
-    const int ch = tid / L, q = tid % L, c = c0 + ch;
-    const bool live = c < p.D;
-    const int lr = tid / S::kPerRow, lc = (tid % S::kPerRow) * E;
-    const int lvalid = lr < kTile ? min(E, p.D - (c0 + lc)) : 0;
+    const int nt = (tend - tbeg + kTile - 1) / kTile;
+    const size_t row0 = (size_t)stream * p.T, part_at = (size_t)stream * p.nseg + g;
 
-    float A[4] = {0.f, 0.f, 0.f, 0.f}, e[4] = {0.f, 0.f, 0.f, 0.f};
-    if (live) {
-        const float4 a = *reinterpret_cast<const float4 *>(p.A + (size_t)c * N + 4 * q);
-        A[0] = a.x; A[1] = a.y; A[2] = a.z; A[3] = a.w;
-    }
-    float A2[4];
+    if (warp < G) {  // ---------------------------------------------------------------- scan
+        const int c = c0 + lane, order = lane & 3;
+        const bool live = c < p.D;
+        float A2[R][4];
+        f32x2 e[R][2], A[R][2], dA[R][2];
+        auto load_state = [&](const float *base, size_t index, int r, f32x2 (&v)[2]) {
+            const float4 a = *reinterpret_cast<const float4 *>(base + (index * p.D + c) * N + 4 * (warp * R + r));
+            float w[4] = {a.x, a.y, a.z, a.w};
+            reorder(w, order);
+            v[0] = pair(w[0], w[1]);
+            v[1] = pair(w[2], w[3]);
+        };
+        auto store_state = [&](float *base, size_t index, int r, const f32x2 (&v)[2]) {
+            float w[4];
+            split(v[0], w[0], w[1]);
+            split(v[1], w[2], w[3]);
+            reorder(w, order);
+            *reinterpret_cast<float4 *>(base + (index * p.D + c) * N + 4 * (warp * R + r)) =
+                make_float4(w[0], w[1], w[2], w[3]);
+        };
+        auto decay = [&](float d, int r, int k) { return pair(ex2(d * A2[r][2 * k]), ex2(d * A2[r][2 * k + 1])); };
 #pragma unroll
-    for (int k = 0; k < 4; ++k) A2[k] = A[k] * kLog2e;
-    auto load_state = [&](const float *base, size_t index, float (&v)[4]) {
-        const float4 a = *reinterpret_cast<const float4 *>(base + (index * p.D + c) * N + 4 * q);
-        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    };
-    auto store_state = [&](float *base, size_t index, const float (&v)[4]) {
-        *reinterpret_cast<float4 *>(base + (index * p.D + c) * N + 4 * q) = make_float4(v[0], v[1], v[2], v[3]);
-    };
-    // e = a_{t+1} dh_{t+1}, the gradient that enters this segment from the right
-    if (live) {
-        if (g == p.nseg - 1) {
-            if (p.dS_T) load_state(p.dS_T, stream, e);
-        } else if (!SUMMARY) {
-            load_state(p.eloc, (size_t)stream * p.nseg + p.nseg - 1, e);
-            for (int i = p.nseg - 2; i > g; --i) {
-                const size_t at = (size_t)stream * p.nseg + i;
-                const float ds = p.dsum[at * p.D + c];
-                float o[4];
-                load_state(p.eloc, at, o);
+        for (int r = 0; r < R; ++r) {
+            e[r][0] = e[r][1] = A[r][0] = A[r][1] = dA[r][0] = dA[r][1] = 0;
+            if (live) load_state(p.A, 0, r, A[r]);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) e[k] = fmaf(ex2(ds * A2[k]), e[k], o[k]);
+            for (int k = 0; k < 2; ++k) {
+                float lo, hi;
+                split(A[r][k], lo, hi);
+                A2[r][2 * k] = lo * kLog2e;
+                A2[r][2 * k + 1] = hi * kLog2e;
+            }
+            // e = a_{t+1} dh_{t+1}, the gradient that enters this segment from the right
+            if (!live) continue;
+            if (g == p.nseg - 1) {
+                if (p.dS_T) load_state(p.dS_T, stream, r, e[r]);
+            } else if (!SUMMARY) {
+                load_state(p.eloc, (size_t)stream * p.nseg + p.nseg - 1, r, e[r]);
+#pragma unroll 2
+                for (int i = p.nseg - 2; i > g; --i) {
+                    const size_t at = (size_t)stream * p.nseg + i;
+                    const float ds = p.dsum[at * p.D + c];
+                    f32x2 o[2];
+                    load_state(p.eloc, at, r, o);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) e[r][k] = fma2(decay(ds, r, k), e[r][k], o[k]);
+                }
             }
         }
+        const float *sdu = smem + S::kDu + 4 * (lane / 2 ^ lane / 16) + 2 * (lane & 1), *sg = smem + S::kG + lane;
+        const float *sbc = smem + S::kBC + 16 * warp * R + 4 * order;
+        float *spart = smem + S::kPart + kCh * warp + lane;
+        // its sum over the channels of one state of B or C; lanes with the same store the same
+        float *ssum = smem + S::kSum + (lane & 4) / 4 * N + 4 * warp * R + order;
+        float dsum = 0.f;
+        f32x2 saved[R][2];  // the state before the next tile
+        auto fetch_saved = [&](int it) {
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                saved[r][0] = saved[r][1] = 0;
+                if (!SUMMARY && live && it >= 0)
+                    load_state(p.saved, (size_t)stream * p.nchunk + tbeg / kTile + it, r, saved[r]);
+            }
+        };
+        fetch_saved(nt - 1);
+        for (int it = nt - 1; it >= 0; --it) {
+            __syncthreads();
+            const int buf = it & 1, t0 = tbeg + it * kTile;
+            auto du_at = [&](int t) { return *reinterpret_cast<const float2 *>(sdu + (buf * kTile + t) * S::kDuRow); };
+            auto g_at = [&](int t) { return sg[(buf * kTile + t) * S::kGRow]; };
+            auto bc_at = [&](int t, int which, int r, f32x2 (&v)[2]) {
+                lds_pairs(sbc + (buf * kTile + t) * S::kBCRow + which * 4 * N + 16 * r, v[0], v[1]);
+            };
+            if constexpr (SUMMARY) {
+#pragma unroll
+                for (int t = kTile - 1; t >= 0; --t) {
+                    const float d = du_at(t).x, gv = g_at(t);
+                    const f32x2 gg = pair(gv, gv);
+                    dsum += d;
+#pragma unroll
+                    for (int r = 0; r < R; ++r) {
+                        f32x2 cc[2];
+                        bc_at(t, 1, r, cc);
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) e[r][k] = mul2(decay(d, r, k), fma2(cc[k], gg, e[r][k]));
+                    }
+                }
+            } else {
+                f32x2 first[R][2];
+#pragma unroll
+                for (int r = 0; r < R; ++r) { first[r][0] = saved[r][0]; first[r][1] = saved[r][1]; }
+                fetch_saved(it - 1);
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    // the compiler reads shared memory anew behind this: it would keep every token's decays for
+                    // the walk back instead of forming them again, in 64 registers
+                    auto forget = [] { asm volatile("" ::: "memory"); };
+                    auto forward = [&](int t, const f32x2 (&from)[2], f32x2 (&to)[2]) {
+                        const float2 du = du_at(t);
+                        const f32x2 uu = pair(du.y, du.y);
+                        f32x2 bb[2];
+                        bc_at(t, 0, r, bb);
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) to[k] = fma2(decay(du.x, r, k), from[k], mul2(uu, bb[k]));
+                    };
+                    struct Token {
+                        float2 du;
+                        float g;
+                        f32x2 b[2], c[2];
+                    };
+                    auto load = [&](int t, Token &k) {
+                        k.du = du_at(t);
+                        k.g = g_at(t);
+                        bc_at(t, 0, r, k.b);
+                        bc_at(t, 1, r, k.c);
+                    };
+                    // the tokens from kFrom on, with the state before them
+                    auto walk = [&](auto from, const f32x2 (&before)[2]) {
+                        constexpr int kFrom = decltype(from)::value;
+                        f32x2 h[kHalf][2];
+                        forward(kFrom, before, h[0]);
+#pragma unroll
+                        for (int i = 1; i < kHalf; ++i) forward(kFrom + i, h[i - 1], h[i]);
+                        forget();
+                        Token now, next;
+                        load(kFrom + kHalf - 1, now);
+#pragma unroll
+                        for (int i = kHalf - 1; i >= 0; --i) {
+                            const int t = kFrom + i;
+                            if (i > 0) load(t - 1, next);
+                            const f32x2 dd = pair(now.du.x, now.du.x), uu = pair(now.du.y, now.du.y);
+                            const f32x2 gg = pair(now.g, now.g);
+                            f32x2 sdx = 0, sdd = 0, sy = 0;
+                            float vb[4], vc[4];
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                const f32x2 prev = i ? h[i ? i - 1 : 0][k] : before[k];
+                                const f32x2 dh = fma2(now.c[k], gg, e[r][k]);
+                                split(mul2(uu, dh), vb[2 * k], vb[2 * k + 1]);
+                                split(mul2(gg, h[i][k]), vc[2 * k], vc[2 * k + 1]);
+                                e[r][k] = mul2(decay(now.du.x, r, k), dh);
+                                const f32x2 m = mul2(e[r][k], prev);
+                                dA[r][k] = fma2(dd, m, dA[r][k]);
+                                sdx = k ? fma2(now.b[k], dh, sdx) : mul2(now.b[k], dh);
+                                sdd = k ? fma2(A[r][k], m, sdd) : mul2(A[r][k], m);
+                                sy = k ? fma2(now.c[k], h[i][k], sy) : mul2(now.c[k], h[i][k]);
+                            }
+                            float *out = spart + (buf * 3 * kTile + t) * S::kPRow;
+                            auto put = [&](int which, f32x2 v) {
+                                float lo, hi;
+                                split(v, lo, hi);
+                                float *o = out + which * kTile * S::kPRow;
+                                *o = r ? *o + (lo + hi) : lo + hi;
+                            };
+                            put(0, sdx);
+                            put(1, sdd);
+                            put(2, sy);
+                            ssum[(buf * kTile + t) * 2 * N + 4 * r] = channel_sum(vb, vc, lane);
+                            now = next;
+                        }
+                    };
+                    f32x2 middle[2] = {first[r][0], first[r][1]};
+#pragma unroll
+                    for (int t = 0; t < kHalf; ++t) forward(t, middle, middle);
+                    forget();
+                    walk(std::integral_constant<int, kHalf>{}, middle);
+                    walk(std::integral_constant<int, 0>{}, first[r]);
+                }
+            }
+        }
+        if constexpr (!SUMMARY) __syncthreads();
+        if (live) {
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                if (SUMMARY || (g == p.nseg - 1 && p.nseg > 1)) store_state(p.eloc, part_at, r, e[r]);
+                if constexpr (!SUMMARY) {
+                    store_state(p.pA, part_at, r, dA[r]);
+                    if (g == 0 && p.dS0) store_state(p.dS0, stream, r, e[r]);
+                }
+            }
+            if (SUMMARY && warp == 0) p.dsum[part_at * p.D + c] = dsum;
+        }
+        if constexpr (!SUMMARY) __syncthreads();
+        return;
     }
-    float bias[E], skip[E];
+    // ---------------------------------------------------------------- helpers
+    const int hid = tid - 32 * G;
+    const int lr = hid / (kCh / E), lc = hid % (kCh / E) * E;  // its token of a tile, its first channel
+    const int lvalid = min(E, p.D - (c0 + lc));
+    float bias[E], skip[E], aD[E], ab[E];
 #pragma unroll
     for (int i = 0; i < E; ++i) {
         bias[i] = p.bias && i < lvalid ? __ldg(p.bias + c0 + lc + i) : 0.f;
         skip[i] = p.Dskip && i < lvalid ? __ldg(p.Dskip + c0 + lc + i) : 0.f;
+        aD[i] = ab[i] = 0.f;
     }
     const T *x = static_cast<const T *>(p.x), *dt = static_cast<const T *>(p.dt), *z = static_cast<const T *>(p.z);
     const T *dy = static_cast<const T *>(p.dy);
-    const T *Bm = static_cast<const T *>(p.Bm), *Cm = static_cast<const T *>(p.Cm);
+    // as in the forward, loads are never conditional: tokens past the segment and channels past D read the
+    // last one, and are made inert when converted
     auto load_run = [&](const T *base, long long ld, int t, Raw<T, E> &r) {
-        if (t >= tend || lvalid <= 0) { r.zero(); return; }
-        const T *src = base + ((size_t)stream * p.T + t) * ld + c0 + lc;
-        if constexpr (VEC) r.load_vec(src);
-        else r.load_each(src, lvalid);
+        const T *row = base + (row0 + min(t, tend - 1)) * ld;
+        if constexpr (VEC) r.load_vec(row + min(c0 + lc, p.D - E));
+        else r.load_clamped(row, c0 + lc, p.D - 1);
     };
-    auto store_run = [&](void *base, int t, const float (&v)[E]) {
-        T *dst = static_cast<T *>(base) + ((size_t)stream * p.T + t) * p.D + c0 + lc;
-        if constexpr (VEC) store_vec<T, E>(dst, v);
-        else store_each<T, E>(dst, v, lvalid);
+    struct Tokens {
+        Raw<T, E> x, dt, z, dy;
+        uint32_t bc[S::kRuns][4];
     };
-    Raw<T, E> rx, rdt, rz, rdy, nx, ndt, nz, ndy;
-    float nb[kBC], nc[kBC];
-    auto fetch = [&](int t0) {
-        load_run(x, p.ldx, t0 + lr, nx);
-        load_run(dt, p.lddt, t0 + lr, ndt);
-        load_run(dy, p.D, t0 + lr, ndy);
-        if (z) load_run(z, p.ldz, t0 + lr, nz);
+    constexpr int kUnits = N / 2;  // runs of B and C of one token
+    const int bu = hid % kUnits, br = hid / kUnits;
+    constexpr int kRows = kHelpers / kUnits;
+    const bool is_c = bu >= N / 4;
+    const T *const bc_base = (is_c ? static_cast<const T *>(p.Cm) : static_cast<const T *>(p.Bm)) + bu % (N / 4) * 4;
+    const long long bc_ld = is_c ? p.ldc : p.ldb;
+    auto fetch = [&](int t0, Tokens &k) {
+        load_run(dt, p.lddt, t0 + lr, k.dt);
+        load_run(dy, p.D, t0 + lr, k.dy);
+        load_run(x, p.ldx, t0 + lr, k.x);
+        if (z) load_run(z, p.ldz, t0 + lr, k.z);
 #pragma unroll
-        for (int i = 0; i < kBC; ++i) {
-            const int r = (tid + i * kThreads) / N, n = (tid + i * kThreads) % N, t = t0 + r;
-            const size_t row = (size_t)stream * p.T + t;
-            nb[i] = r < kTile && t < tend ? load_one(Bm + row * p.ldb + n) : 0.f;
-            nc[i] = r < kTile && t < tend ? load_one(Cm + row * p.ldc + n) : 0.f;
+        for (int i = 0; i < S::kRuns; ++i) {
+            const T *b = bc_base + (row0 + min(t0 + br + i * kRows, tend - 1)) * bc_ld;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) k.bc[i][j] = load_bits(b + j);
         }
     };
-    float dA[4] = {0.f, 0.f, 0.f, 0.f}, dsum = 0.f;
-    float aD[E], ab[E];
+    auto keep_at = [&](int it, int what) {  // four floats of this thread, of one tile
+        return reinterpret_cast<float4 *>(smem + S::kKeep) + ((it % 3) * 5 + what) * kHelpers + hid;
+    };
+    auto convert = [&](const Tokens &tok, int it) {
+        const int t0 = tbeg + it * kTile, buf = it & 1;
+        const bool in = t0 + lr < tend;
+        float d[E], sg[E], xv[E], gv[E], zf[E];
 #pragma unroll
-    for (int i = 0; i < E; ++i) aD[i] = ab[i] = 0.f;
-    const int nt = (tend - tbeg + kTile - 1) / kTile;
-    fetch(tbeg + (nt - 1) * kTile);
+        for (int i = 0; i < E; ++i) {
+            d[i] = tok.dt.get(i) + bias[i];
+            xv[i] = tok.x.get(i);
+            gv[i] = tok.dy.get(i);
+            sg[i] = 1.f;
+            zf[i] = 0.f;
+        }
+        if (p.softplus)
+#pragma unroll
+            for (int i = 0; i < E; ++i) { sg[i] = sigmoid(d[i]); d[i] = softplus(d[i]); }
+        if (z)
+#pragma unroll
+            for (int i = 0; i < E; ++i) {
+                const float zv = tok.z.get(i), s = sigmoid(zv);
+                zf[i] = gv[i] * s * fmaf(zv, 1.f - s, 1.f);
+                gv[i] *= zv * s;
+            }
+        float u[E];
+#pragma unroll
+        for (int i = 0; i < E; ++i) u[i] = d[i] * xv[i];
+        if (t0 + kTile > tend || lvalid < E)
+#pragma unroll
+            for (int i = 0; i < E; ++i)
+                if (!in || i >= lvalid) d[i] = u[i] = gv[i] = 0.f;
+        const int swap = lc / (kCh / 2);
+        float4 *dst = reinterpret_cast<float4 *>(smem + S::kDu + (buf * kTile + lr) * S::kDuRow + 2 * lc);
+        dst[swap] = make_float4(d[0], u[0], d[1], u[1]);
+        dst[1 - swap] = make_float4(d[2], u[2], d[3], u[3]);
+        auto four = [](const float (&v)[E]) { return make_float4(v[0], v[1], v[2], v[3]); };
+        *reinterpret_cast<float4 *>(smem + S::kG + (buf * kTile + lr) * S::kGRow + lc) = four(gv);
+        if constexpr (!SUMMARY) {
+            *keep_at(it, 0) = four(d);
+            *keep_at(it, 1) = four(gv);
+            *keep_at(it, 2) = four(xv);
+            *keep_at(it, 3) = four(sg);
+            *keep_at(it, 4) = four(zf);
+        }
+#pragma unroll
+        for (int i = 0; i < S::kRuns; ++i) {
+            const int r = br + i * kRows;
+            if (r >= kTile) continue;
+            const bool m = t0 + r < tend;
+            float v[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] = m ? bits_value<T>(tok.bc[i][j]) : 0.f;
+            // order j holds v[k ^ j]; neighbours write different j at a time, and so different banks
+            float4 *o = reinterpret_cast<float4 *>(smem + S::kBC + (buf * kTile + r) * S::kBCRow) + 4 * bu;
+            const int sw = bu / 2 & 3;
+            reorder(v, sw);
+            o[sw] = make_float4(v[0], v[1], v[2], v[3]);
+            o[sw ^ 1] = make_float4(v[1], v[0], v[3], v[2]);
+            o[sw ^ 2] = make_float4(v[2], v[3], v[0], v[1]);
+            o[sw ^ 3] = make_float4(v[3], v[2], v[1], v[0]);
+        }
+    };
+    auto finish = [&](int it) {
+#pragma unroll
+        for (int i = hid; i < kTile * N / 2; i += kHelpers) {  // the tile's sums over channels
+            const int r = i / (N / 2), t = tbeg + it * kTile + r;
+            const float4 v = *reinterpret_cast<const float4 *>(smem + S::kSum + (it & 1) * kTile * 2 * N + 4 * i);
+            if (t < tend)
+                *reinterpret_cast<float4 *>(p.pBC + ((size_t)cb * p.B * p.T + row0 + t) * 2 * N + i % (N / 2) * 4) = v;
+        }
+        const int t = tbeg + it * kTile + lr;
+        if (t >= tend || lvalid <= 0) return;
+        float s[3][E];
+#pragma unroll
+        for (int w = 0; w < 3; ++w) {
+            const float *src = smem + S::kPart + (((it & 1) * 3 + w) * kTile + lr) * S::kPRow + lc;
+#pragma unroll
+            for (int i = 0; i < E; ++i) s[w][i] = 0.f;
+#pragma unroll
+            for (int k = 0; k < G; ++k) {
+                const float4 v = *reinterpret_cast<const float4 *>(src + k * kCh);
+                s[w][0] += v.x; s[w][1] += v.y; s[w][2] += v.z; s[w][3] += v.w;
+            }
+        }
+        float d[E], gv[E], xv[E], sg[E], zf[E];
+        auto get = [&](int what, float (&v)[E]) {
+            const float4 a = *keep_at(it, what);
+            v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+        };
+        get(0, d); get(1, gv); get(2, xv); get(3, sg); get(4, zf);
+        float odx[E], odt[E], oz[E];
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+            odx[i] = fmaf(d[i], s[0][i], skip[i] * gv[i]);
+            odt[i] = fmaf(xv[i], s[0][i], s[1][i]) * sg[i];
+            oz[i] = zf[i] * fmaf(skip[i], xv[i], s[2][i]);
+            if (i < lvalid) {
+                aD[i] = fmaf(gv[i], xv[i], aD[i]);
+                ab[i] += odt[i];
+            }
+        }
+        auto store_run = [&](void *base, const float (&v)[E]) {
+            T *dst = static_cast<T *>(base) + (row0 + t) * p.D + c0 + lc;
+            if constexpr (VEC) store_vec<T, E>(dst, v);
+            else store_each<T, E>(dst, v, lvalid);
+        };
+        store_run(p.dx, odx);
+        store_run(p.ddt, odt);
+        if (z) store_run(p.dz, oz);
+    };
+    // the eight helpers of a token ask for the rows of the six inputs, kAhead tiles before their loads
+    constexpr int kAhead = 3;
+    const T *prow = x + c0;
+    long long prl = p.ldx;
+    switch (hid % 8) {
+    case 1: prow = dt + c0; prl = p.lddt; break;
+    case 2: if (z) { prow = z + c0; prl = p.ldz; } break;
+    case 3: prow = dy + c0; prl = p.D; break;
+    case 4: prow = static_cast<const T *>(p.Bm); prl = p.ldb; break;
+    case 5: prow = static_cast<const T *>(p.Cm); prl = p.ldc; break;
+    }
+    auto prefetch = [&](int t0) {
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(prow + (row0 + max(t0 + lr, tbeg)) * prl));
+    };
+    Tokens tok;
+    if (nt > 0) {
+#pragma unroll
+        for (int k = 1; k <= kAhead && k < nt; ++k) prefetch(tbeg + (nt - 1 - k) * kTile);
+        fetch(tbeg + (nt - 1) * kTile, tok);
+        convert(tok, nt - 1);
+        if (nt > 1) fetch(tbeg + (nt - 2) * kTile, tok);
+    }
     for (int it = nt - 1; it >= 0; --it) {
-        const int t0 = tbeg + it * kTile;
-        rx = nx; rdt = ndt; rz = nz; rdy = ndy;
-        const bool run_ok = t0 + lr < tend && lvalid > 0;
-#pragma unroll
-        for (int i = 0; i < E && lr < kTile; ++i) {
-            const float v = rdt.get(i) + bias[i];
-            const float d = run_ok && i < lvalid ? (p.softplus ? softplus(v) : v) : 0.f;
-            float gv = rdy.get(i);
-            if (z) { const float zv = rz.get(i); gv *= zv * sigmoid(zv); }
-            sdx[lr * kRow + lc + i] = make_float2(d, d * rx.get(i));
-            sg[lr * kRow + lc + i] = gv;  // zero past the segment and past D (dy was filled with zeros)
-        }
-#pragma unroll
-        for (int i = 0; i < kBC; ++i) {
-            const int at = tid + i * kThreads;
-            if (at < kTile * N) { sB[at] = nb[i]; sC[at] = nc[i]; }
-        }
         __syncthreads();
-        if (it > 0) fetch(t0 - kTile);
-        if constexpr (SUMMARY) {
+        if (it > 0) convert(tok, it - 1);
+        if (!SUMMARY && it < nt - 1) finish(it + 1);
+        if (it > 1) fetch(tbeg + (it - 2) * kTile, tok);
+        if (it > 1 + kAhead) prefetch(tbeg + (it - 2 - kAhead) * kTile);
+    }
+    if constexpr (!SUMMARY) {
+        __syncthreads();
+        if (nt > 0) finish(0);
+        // the tokens' parts of dDskip and dbias of each channel, through shared memory
+        float4 *sd = reinterpret_cast<float4 *>(smem + S::kBC), *sb = sd + kHelpers;
+        sd[hid] = make_float4(aD[0], aD[1], aD[2], aD[3]);
+        sb[hid] = make_float4(ab[0], ab[1], ab[2], ab[3]);
+        __syncthreads();
+        if (hid < 2 * kCh) {
+            const float *src = reinterpret_cast<const float *>(hid < kCh ? sd : sb) + hid % kCh;
+            float s = 0.f;
 #pragma unroll
-            for (int t = kTile - 1; t >= 0; --t) {
-                const float d = sdx[t * kRow + ch].x, gv = sg[t * kRow + ch];
-                const float4 cv = *reinterpret_cast<const float4 *>(sC + t * N + 4 * q);
-                dsum += d;
-                e[0] = ex2(d * A2[0]) * fmaf(cv.x, gv, e[0]);
-                e[1] = ex2(d * A2[1]) * fmaf(cv.y, gv, e[1]);
-                e[2] = ex2(d * A2[2]) * fmaf(cv.z, gv, e[2]);
-                e[3] = ex2(d * A2[3]) * fmaf(cv.w, gv, e[3]);
-            }
-            __syncthreads();
-        } else {
-            float h0[4] = {0.f, 0.f, 0.f, 0.f}, hist[kTile][4];
-            if (live) load_state(p.saved, (size_t)stream * p.nchunk + t0 / kTile, h0);
-#pragma unroll
-            for (int t = 0; t < kTile; ++t) {
-                const float2 dx = sdx[t * kRow + ch];
-                const float4 b = *reinterpret_cast<const float4 *>(sB + t * N + 4 * q);
-                const float bb[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float prev = t ? hist[t ? t - 1 : 0][k] : h0[k];
-                    hist[t][k] = fmaf(ex2(dx.x * A2[k]), prev, dx.y * bb[k]);
-                }
-            }
-#pragma unroll
-            for (int t = kTile - 1; t >= 0; --t) {
-                const float2 dx = sdx[t * kRow + ch];
-                const float gv = sg[t * kRow + ch];
-                const float4 b = *reinterpret_cast<const float4 *>(sB + t * N + 4 * q);
-                const float4 cv = *reinterpret_cast<const float4 *>(sC + t * N + 4 * q);
-                const float bb[4] = {b.x, b.y, b.z, b.w}, cc[4] = {cv.x, cv.y, cv.z, cv.w};
-                float v[8], du = 0.f, dd = 0.f;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float prev = t ? hist[t ? t - 1 : 0][k] : h0[k];
-                    const float a = ex2(dx.x * A2[k]);
-                    const float dh = fmaf(cc[k], gv, e[k]);
-                    v[k] = dx.y * dh;
-                    v[4 + k] = gv * hist[t][k];
-                    du = fmaf(bb[k], dh, du);
-                    e[k] = a * dh;
-                    const float m = e[k] * prev;
-                    dd = fmaf(A[k], m, dd);
-                    dA[k] = fmaf(dx.x, m, dA[k]);
-                }
-                du = lane_sum<L>(du);
-                dd = lane_sum<L>(dd);
-                if (q == 0) sdx[t * kRow + ch] = make_float2(du, dd);  // after every lane's reads of this slot
-                if (z) {
-                    float yv = fmaf(cc[0], hist[t][0], cc[1] * hist[t][1]) + fmaf(cc[2], hist[t][2], cc[3] * hist[t][3]);
-                    yv = lane_sum<L>(yv);
-                    if (q == 0) sy[t * kRow + ch] = yv;
-                }
-                int at;
-                ChannelSum<L>::run(v, lane, at);
-                // value index j of a lane: j < 4 is dB of state 4 q + j, else dC of 4 q + j - 4
-                if (L > 2 || lane < 16)
-#pragma unroll
-                    for (int i = 0; i < ChannelSum<L>::kLeft; ++i) {
-                        const int j = at + i;
-                        sred[(warp * kTile + t) * 2 * N + (j < 4 ? 0 : N) + 4 * q + (j & 3)] = v[i];
-                    }
-            }
-            __syncthreads();
-            if (run_ok) {
-                float odx[E], odt[E], oz[E];
-#pragma unroll
-                for (int i = 0; i < E; ++i) {
-                    const int at = lr * kRow + lc + i;
-                    const float2 s = sdx[at];
-                    const float v = rdt.get(i) + bias[i], xv = rx.get(i), gv = sg[at];
-                    const float d = p.softplus ? softplus(v) : v;
-                    odx[i] = fmaf(d, s.x, skip[i] * gv);
-                    float dd = fmaf(xv, s.x, s.y);
-                    if (p.softplus) dd *= sigmoid(v);
-                    odt[i] = dd;
-                    aD[i] = fmaf(gv, xv, aD[i]);
-                    ab[i] += dd;
-                    if (z) {
-                        const float zv = rz.get(i), s1 = sigmoid(zv);
-                        oz[i] = rdy.get(i) * fmaf(skip[i], xv, sy[at]) * s1 * fmaf(zv, 1.f - s1, 1.f);
-                    }
-                }
-                store_run(p.dx, t0 + lr, odx);
-                store_run(p.ddt, t0 + lr, odt);
-                if (z) store_run(p.dz, t0 + lr, oz);
-            }
-            for (int i = tid; i < kTile * 2 * N; i += kThreads) {
-                const int t = t0 + i / (2 * N);
-                float s = 0.f;
-#pragma unroll
-                for (int w = 0; w < S::kWarps; ++w) s += sred[w * kTile * 2 * N + i];
-                if (t < tend) p.pBC[(((size_t)cb * p.B + stream) * p.T + t) * 2 * N + i % (2 * N)] = s;
-            }
-            __syncthreads();
+            for (int r = 0; r < kTile; ++r) s += src[r * kCh];
+            const int c = c0 + hid % kCh;
+            if (c < p.D) p.pD[(part_at * 2 + hid / kCh) * p.D + c] = s;
         }
     }
-    const size_t at = (size_t)stream * p.nseg + g;
-    if constexpr (SUMMARY) {
-        if (!live) return;
-        store_state(p.eloc, at, e);
-        if (q == 0) p.dsum[at * p.D + c] = dsum;
+}
+
+// FIRST (two segments or more): the last segment whole and the others' summaries, from the second on;
+// otherwise all segments (one), or those up to the last but one.
+template <typename T, int N, bool VEC, bool FIRST>
+__global__ void __launch_bounds__(BwdShape<N>::kBlock, BwdShape<N>::kBlocks) ssm_backward_kernel(BwdParams p)
+{
+    extern __shared__ __align__(16) float smem[];
+    if constexpr (FIRST) {
+        if (blockIdx.y == 0) walk_segment<T, N, VEC, false>(p, p.nseg - 1, smem);
+        else walk_segment<T, N, VEC, true>(p, blockIdx.y, smem);
     } else {
-        if (live) {
-            store_state(p.pA, at, dA);
-            if (g == 0 && p.dS0) store_state(p.dS0, stream, e);
-        }
-        // the 16 tokens' parts of dDskip and dbias of each channel, through shared memory
-        float *sd = reinterpret_cast<float *>(sdx);
-#pragma unroll
-        for (int i = 0; i < E && lr < kTile; ++i) {
-            sd[lr * kRow + lc + i] = aD[i];
-            sg[lr * kRow + lc + i] = ab[i];
-        }
-        __syncthreads();
-        for (int i = tid; i < 2 * CH; i += kThreads) {
-            const int cc = i % CH;
-            const float *src = i < CH ? sd : sg;
-            float s = 0.f;
-            for (int r = 0; r < kTile; ++r) s += src[r * kRow + cc];
-            if (c0 + cc < p.D) p.pD[(at * 2 + i / CH) * p.D + c0 + cc] = s;
-        }
+        walk_segment<T, N, VEC, false>(p, blockIdx.y, smem);
     }
 }
 
@@ -345,6 +517,7 @@ __global__ void ssm_reduce_bc_kernel(const float *pBC, long long rows, int N, in
     const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x, n = rows * 2 * N;
     if (i >= n) return;
     float s = 0.f;
+#pragma unroll 8
     for (int b = 0; b < ncb; ++b) s += pBC[b * n + i];
     const long long row = i / (2 * N);
     const int j = (int)(i % (2 * N));
@@ -380,15 +553,14 @@ template <typename T, int N>
 cudaError_t launch_bwd(const SsmArgs &a, const SsmGrads &g, const BwdParams &p, cudaStream_t st)
 {
     using S = BwdShape<N>;
-    const int bytes = S::E * (int)sizeof(T) < 16 ? S::E * (int)sizeof(T) : 16;
-    auto ok = [&](const void *q, long long ld) { return runs_aligned(q, ld, sizeof(T), bytes); };
-    const bool vec = a.D % S::E == 0 && bytes >= 4 && ok(a.x, a.ldx) && ok(a.dt, a.lddt) && ok(a.z, a.ldz) &&
-                     ok(g.dy, a.D) && ok(g.dx, a.D) && ok(g.ddt, a.D) && ok(g.dz, a.D);
+    auto ok = [&](const void *q, long long ld) { return runs_aligned(q, ld, sizeof(T), E * (int)sizeof(T)); };
+    const bool vec = a.D % E == 0 && ok(a.x, a.ldx) && ok(a.dt, a.lddt) && ok(a.z, a.ldz) && ok(g.dy, a.D) &&
+                     ok(g.dx, a.D) && ok(g.ddt, a.D) && ok(g.dz, a.D);
     auto run = [&](auto *kern, int segments) -> cudaError_t {
         const int smem = S::kFloats * (int)sizeof(float);
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
-        kern<<<dim3(p.ncb * a.B, segments), kThreads, smem, st>>>(p);
+        kern<<<dim3(p.ncb * a.B, segments), S::kBlock, smem, st>>>(p);
         return cudaGetLastError();
     };
     cudaError_t e = cudaSuccess;
@@ -396,7 +568,8 @@ cudaError_t launch_bwd(const SsmArgs &a, const SsmGrads &g, const BwdParams &p, 
         e = vec ? run(ssm_backward_kernel<T, N, true, true>, p.nseg - 1)
                 : run(ssm_backward_kernel<T, N, false, true>, p.nseg - 1);
     if (e != cudaSuccess) return e;
-    e = vec ? run(ssm_backward_kernel<T, N, true, false>, p.nseg) : run(ssm_backward_kernel<T, N, false, false>, p.nseg);
+    const int rest = p.nseg > 1 ? p.nseg - 1 : 1;
+    e = vec ? run(ssm_backward_kernel<T, N, true, false>, rest) : run(ssm_backward_kernel<T, N, false, false>, rest);
     if (e != cudaSuccess) return e;
     const long long rows = (long long)a.B * a.T, nbc = rows * 2 * N;
     ssm_reduce_bc_kernel<T><<<(unsigned)((nbc + 255) / 256), 256, 0, st>>>(p.pBC, rows, N, p.ncb,
@@ -421,14 +594,49 @@ cudaError_t launch_bwd_n(const SsmArgs &a, const SsmGrads &g, const BwdParams &p
     }
 }
 
+int sm_count()
+{
+    int dev = 0, n = 148;
+    if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+    return n > 0 ? n : 148;
+}
+
+// Segments of the time axis, as in the forward. Of two launches the first runs a whole segment and g - 2 summaries
+// per 32 channels, the second g - 1 whole ones; a summary costs kSummary of a whole token.
+SsmSplit ssm_backward_split(int streams, int T, int D, int N)
+{
+    constexpr double kAlone = 1.27, kSummary = 0.45;
+    const long long blocks = (long long)streams * ((D + kCh - 1) / kCh);
+    const int sms = sm_count(), tiles = (T + kTile - 1) / kTile;
+    auto load = [&](long long n) {  // of n equal blocks, in tokens of one of two blocks that share an SM
+        const long long k = (n + sms - 1) / sms;
+        return k % 2 ? k - 1 + kAlone : (double)k;
+    };
+    auto cost = [&](int g) {
+        const double tokens = (tiles + g - 1) / g * (double)kTile + 32.;
+        if (g == 1) return tokens * load(blocks);
+        const double f = (1. + kSummary * (g - 2)) / (g - 1);  // a first launch's block, on average
+        return tokens * load(blocks * (g - 1)) * (1. + (f < kSummary ? kSummary : f)) + 2. * g;
+    };
+    int best = 1;
+    for (int g = 2; g <= tiles && g <= 256; ++g)
+        if (cost(g) < cost(best)) best = g;
+    SsmSplit s;
+    s.seg = (tiles + best - 1) / best * kTile;
+    if (s.seg < kTile) s.seg = kTile;
+    s.nseg = (T + s.seg - 1) / s.seg;
+    if (s.nseg < 1) s.nseg = 1;
+    return s;
+}
+
 // The backward's workspace, in this order; every part starts on 256 bytes.
 struct Layout {
     size_t scan, saved, eloc, dsum, pBC, pA, pD, total;
 };
 Layout layout(int B, int T, int D, int N, bool have_saved)
 {
-    const SsmSplit s = ssm_split(B, T, D, N);
-    const size_t ncb = (size_t)(D + 1024 / N - 1) / (1024 / N), parts = (size_t)B * s.nseg;
+    const SsmSplit s = ssm_backward_split(B, T, D, N);
+    const size_t ncb = (size_t)(D + kCh - 1) / kCh, parts = (size_t)B * s.nseg;
     const size_t nchunk = (size_t)(T + kSsmChunk - 1) / kSsmChunk;
     size_t at = 0;
     auto take = [&](size_t floats) { const size_t r = at; at += (floats * 4 + 255) / 256 * 256; return r; };
@@ -468,11 +676,11 @@ cudaError_t launch_ssm_backward(const SsmArgs &a, const SsmGrads &g, cudaStream_
         if (e != cudaSuccess) return e;
         saved = f.saved_states;
     }
-    const SsmSplit s = ssm_split(a.B, a.T, a.D, a.N);
+    const SsmSplit s = ssm_backward_split(a.B, a.T, a.D, a.N);
     BwdParams p;
     p.B = a.B; p.T = a.T; p.D = a.D; p.seg = s.seg; p.nseg = s.nseg;
     p.nchunk = (a.T + kSsmChunk - 1) / kSsmChunk;
-    p.ncb = (a.D + 1024 / a.N - 1) / (1024 / a.N);
+    p.ncb = (a.D + kCh - 1) / kCh;
     p.softplus = a.softplus;
     p.x = a.x; p.dt = a.dt; p.z = a.z; p.Bm = a.Bm; p.Cm = a.Cm; p.dy = g.dy;
     p.ldx = a.ldx; p.lddt = a.lddt; p.ldz = a.ldz; p.ldb = a.ldb; p.ldc = a.ldc;

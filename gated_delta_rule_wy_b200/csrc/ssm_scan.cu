@@ -533,24 +533,6 @@ SsmSplit ssm_scan_split(int streams, int T, int D, int N)
     return s;
 }
 
-// Segments of the backward: enough blocks to fill the GPU four times over, segments of at
-// least 64 tokens, and none where the channels alone give two blocks per SM.
-SsmSplit ssm_split(int streams, int T, int D, int N)
-{
-    const long long blocks = (long long)streams * ((D + 1024 / N - 1) / (1024 / N));
-    const int sms = sm_count();
-    long long g = blocks >= 2LL * sms ? 1 : (4LL * sms + blocks - 1) / (blocks > 0 ? blocks : 1);
-    const long long most = (T + 63) / 64;
-    if (g > most) g = most;
-    if (g < 1) g = 1;
-    SsmSplit s;
-    s.seg = (int)(((T + g - 1) / g + kSsmChunk - 1) / kSsmChunk * kSsmChunk);
-    if (s.seg < kSsmChunk) s.seg = kSsmChunk;
-    s.nseg = (T + s.seg - 1) / s.seg;
-    if (s.nseg < 1) s.nseg = 1;
-    return s;
-}
-
 size_t ssm_scan_workspace_bytes(int streams, int T, int D, int N)
 {
     const SsmSplit s = ssm_scan_split(streams, T, D, N);
