@@ -158,24 +158,37 @@ def _one_device(fn):
     """
     @functools.wraps(fn)
     def call(*args, **kwargs):
-        dev = _device_of(_tensors_in(args, kwargs))
+        dev = None
+        for group in (args, kwargs.values()):
+            for a in group:
+                if isinstance(a, torch.Tensor):
+                    if dev is None:
+                        dev = a.device
+                    elif a.device != dev:
+                        _device_of(_tensors_in(args, kwargs))
+                elif isinstance(a, (list, tuple)):
+                    dev = _device_of(_tensors_in(args, kwargs))
         if dev is None or dev.type != "cuda":
             return fn(*args, **kwargs)  # the argument checks reject host tensors
         stream = kwargs.get("stream")
         if stream is not None and stream.device != dev:
             raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}: one CUDA device per call")
+        if torch.cuda.current_device() == dev.index:
+            return fn(*args, **kwargs)
         with torch.cuda.device(dev):
             return fn(*args, **kwargs)
     return call
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream=None):
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    """The raw stream, the current one of the current device unless one is given."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream
 
 
 def _dt(t: torch.Tensor) -> int:
@@ -193,7 +206,7 @@ def _check(t, name, shape, dtype):
         raise ValueError(f"{name} must be a CUDA tensor")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.dtype != dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
@@ -458,13 +471,12 @@ def gdr2_short_conv_silu_backward(x, weight, dy, state=None, dstate_out=None, *,
     _check(state, "state", (N, W - 1, H, d), dt)
     _check(dstate_out, "dstate_out", (N, W - 1, H, d), dt)
     want = state is not None if want_dstate is None else want_dstate
-    g = {"dx": torch.empty_like(x), "dweight": torch.empty(tuple(weight.shape), dtype=torch.float32, device=x.device),
-         "dstate": torch.empty((N, W - 1, H, d), dtype=dt, device=x.device) if want else None}
+    g = {"dx": torch.empty_like(x), "dweight": _like(weight), "dstate": x.new_empty((N, W - 1, H, d)) if want else None}
     if N * H == 0:
         g["dweight"].zero_()
     need = lib.gdr2_short_conv_silu_backward_workspace_bytes(N, T, H, d, W)
     workspace = _workspace(workspace, need, x.device)
-    st = lib.gdr2_short_conv_silu_backward(N, T, H, d, _dt(x), W, int(bool(l2norm)), ctypes.c_float(eps), _some(x),
+    st = lib.gdr2_short_conv_silu_backward(N, T, H, d, _dt(x), W, int(bool(l2norm)), eps, _some(x),
                                            _some(wgt), _some(state), _some(dy), _some(dstate_out), _some(g["dx"]),
                                            _some(g["dweight"]), _some(g["dstate"]), _some(workspace),
                                            _nbytes(workspace), _stream(stream))
@@ -474,11 +486,16 @@ def gdr2_short_conv_silu_backward(x, weight, dy, state=None, dstate_out=None, *,
 
 def _some(t):
     """The data pointer, or NULL for None and for a tensor without elements."""
-    return None if t is None or t.numel() == 0 else _ptr(t)
+    return None if t is None or t.numel() == 0 else t.data_ptr()
 
 
 def _nbytes(t):
-    return ctypes.c_size_t(0 if t is None else t.numel() * t.element_size())
+    return 0 if t is None else t.numel() * t.element_size()
+
+
+def _like(t):
+    """An uninitialised contiguous tensor of t's shape, dtype and device."""
+    return torch.empty_like(t) if t.is_contiguous() else t.new_empty(t.shape)
 
 
 def _workspace(given, need, device):
@@ -497,19 +514,27 @@ def _rows(t, name, lead, width, dtype):
         return 0
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if tuple(t.shape) != (*lead, width):
+    if t.shape != (*lead, width):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(*lead, width)}")
     if t.dtype != dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if t.numel() == 0:
+    if t.is_contiguous():  # so is a tensor without elements
         return width
-    if width > 1 and t.stride(-1) != 1:
+    strides = t.stride()
+    if width > 1 and strides[-1] != 1:
         raise ValueError(f"{name} must be dense in its last dimension")
+    return _row_distance(name, lead, strides, width)
+
+
+def _row_distance(name, lead, strides, width):
+    """The one distance between rows of `width` elements over the leading dimensions, or a refusal."""
     ld, rows = None, 1  # distance between rows; the rows that the dimensions from here on hold
-    for n, s in reversed(list(zip(lead, t.stride()[:-1]))):
+    for i in range(len(lead) - 1, -1, -1):
+        n = lead[i]
         if n > 1:
-            ld = s if ld is None else ld
-            if s != ld * rows:
+            if ld is None:
+                ld = strides[i]
+            if strides[i] != ld * rows:
                 raise ValueError(f"the rows of {name} must all be the same distance apart")
         rows *= n
     ld = width if ld is None else ld
@@ -524,18 +549,15 @@ def _ssm_inputs(x, dt, A, Bm, Cm, D, z, dt_bias, packed=None):
     lead, C = tuple(x.shape[:-1]), x.shape[-1]
     N = A.shape[-1]
     t = x.dtype
-    lds = [_rows(v, n, lead, w, t) for v, n, w in ((x, "x", C), (dt, "dt", C), (Bm, "Bm", N), (Cm, "Cm", N),
-                                                    (z, "z", C))]
+    ldx, ldt = _rows(x, "x", lead, C, t), _rows(dt, "dt", lead, C, t)
+    ldb, ldc, ldz = _rows(Bm, "Bm", lead, N, t), _rows(Cm, "Cm", lead, N, t), _rows(z, "z", lead, C, t)
     _check(A, "A", (C, N), torch.float32)
     _check(D, "D", (C,), torch.float32)
     _check(dt_bias, "dt_bias", (C,), torch.float32)
     if packed is not None:
         _check_cu_seqlens(packed, x.device)
-    for v, n in ((dt, "dt"), (A, "A"), (Bm, "Bm"), (Cm, "Cm"), (D, "D"), (z, "z"), (dt_bias, "dt_bias")):
-        if v is not None and v.device != x.device:
-            raise ValueError(f"{n} must be on x's device")
-    args = [_some(x), lds[0], _some(dt), lds[1], _some(A), _some(Bm), lds[2], _some(Cm), lds[3], _some(D), _some(z),
-            lds[4], _some(dt_bias)]
+    args = (_some(x), ldx, _some(dt), ldt, _some(A), _some(Bm), ldb, _some(Cm), ldc, _some(D), _some(z), ldz,
+            _some(dt_bias))
     return lead, C, N, t, args
 
 
@@ -559,12 +581,12 @@ def gdr2_ssm_scan(x, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, S0=None, *, so
     B = lead[0] if cu_seqlens is None else cu_seqlens.numel() - 1
     dev = x.device
     _check(S0, "S0", (B, C, N), torch.float32)
-    y = out if out is not None else torch.empty((*lead, C), dtype=t, device=dev)
-    _check(y, "out", (*lead, C), t)
-    S_T = torch.empty((B, C, N), dtype=torch.float32, device=dev) if final_state else None
+    y = _like(x) if out is None else out
+    _check(out, "out", x.shape, t)
+    S_T = A.new_empty((B, C, N)) if final_state else None
     if save_states and cu_seqlens is not None:
         raise ValueError("save_states is for dense sequences (the backward takes no cu_seqlens)")
-    saved = torch.empty((B, -(-T // SSM_CHUNK), C, N), dtype=torch.float32, device=dev) if save_states else None
+    saved = A.new_empty((B, -(-T // SSM_CHUNK), C, N)) if save_states else None
     need = lib.gdr2_ssm_scan_workspace_bytes(B if cu_seqlens is None else 1, T, C, N)
     workspace = _workspace(workspace, need, dev)
     st = lib.gdr2_ssm_scan(B, T, C, N, _dt(x), int(bool(softplus)), _ptr(cu_seqlens), *args, _some(S0), _some(y),
@@ -582,8 +604,8 @@ def gdr2_ssm_step(x, dt, A, Bm, Cm, S, D=None, z=None, dt_bias=None, *, softplus
     if len(lead) != 1:
         raise ValueError("x must be [B, C]")
     _check(S, "S", (*lead, C, N), torch.float32)
-    y = out if out is not None else torch.empty((*lead, C), dtype=t, device=x.device)
-    _check(y, "out", (*lead, C), t)
+    y = _like(x) if out is None else out
+    _check(out, "out", x.shape, t)
     st = lib.gdr2_ssm_step(lead[0], C, N, _dt(x), int(bool(softplus)), *args, _some(S), _some(y), _stream(stream))
     _raise(lib, st)
     return y
@@ -604,11 +626,10 @@ def gdr2_ssm_scan_backward(x, dt, A, Bm, Cm, dy, D=None, z=None, dt_bias=None, S
     _check(S0, "S0", (B, C, N), torch.float32)
     _check(dS_T, "dS_T", (B, C, N), torch.float32)
     _check(saved_states, "saved_states", (B, -(-T // SSM_CHUNK), C, N), torch.float32)
-    f32 = lambda *s: torch.empty(s, dtype=torch.float32, device=dev)  # noqa: E731
-    own = lambda *s: torch.empty(s, dtype=t, device=dev)  # noqa: E731
-    g = {"dx": own(B, T, C), "ddt": own(B, T, C), "dA": f32(C, N), "dBm": own(B, T, N), "dCm": own(B, T, N),
-         "dD": None if D is None else f32(C), "dz": None if z is None else own(B, T, C),
-         "ddt_bias": None if dt_bias is None else f32(C), "dS0": f32(B, C, N) if want_dS0 else None}
+    g = {"dx": _like(x), "ddt": _like(dt), "dA": _like(A), "dBm": _like(Bm), "dCm": _like(Cm),
+         "dD": None if D is None else _like(D), "dz": None if z is None else _like(z),
+         "ddt_bias": None if dt_bias is None else _like(dt_bias),
+         "dS0": A.new_empty((B, C, N)) if want_dS0 else None}
     need = lib.gdr2_ssm_scan_backward_workspace_bytes(B, T, C, N, int(saved_states is not None))
     workspace = _workspace(workspace, need, dev)
     st = lib.gdr2_ssm_scan_backward(B, T, C, N, _dt(x), int(bool(softplus)), *args, _some(S0), _some(dy), _some(dS_T),
@@ -622,18 +643,32 @@ def gdr2_ssm_scan_backward(x, dt, A, Bm, Cm, dy, D=None, z=None, dt_bias=None, S
 _NORMS = {None: 0, "rms": 1, "l2": 2}
 
 
+def _head_rows(v, name, shape, dtype):
+    """As _rows, of tokens of heads that lie dense and side by side."""
+    if v is None:
+        return 0
+    if not v.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if v.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(v.shape)}, expected {shape}")
+    if v.dtype != dtype:
+        raise TypeError(f"{name} has dtype {v.dtype}, expected {dtype}")
+    H, d = shape[2:]
+    if v.is_contiguous():
+        return H * d
+    strides = v.stride()
+    if strides[-1] != 1 or (H > 1 and strides[-2] != d):
+        raise ValueError(f"the heads of {name} must be dense and side by side")
+    return _row_distance(name, shape[:2], strides, H * d)
+
+
 def _rope_inputs(q, k, q_weight, k_weight, cos_sin, positions, norm, eps, interleaved, first_position):
     if norm not in _NORMS:
         raise ValueError(f"norm must be 'rms', 'l2' or None, not {norm!r}")
     B, T, Hq, d = q.shape
     Hk = 0 if k is None else k.shape[2]
     t = q.dtype
-    lds = []
-    for v, n, H in ((q, "q", Hq), (k, "k", Hk)):
-        if v is not None and v.numel() and (v.stride(-1) != 1 or (H > 1 and v.stride(-2) != d)):
-            raise ValueError(f"the heads of {n} must be dense and side by side")
-        lds.append(0 if v is None else _rows(v.flatten(-2) if v.numel() else v.reshape(B, T, H * d), n, (B, T), H * d,
-                                             t))
+    ldq, ldk = _head_rows(q, "q", (B, T, Hq, d), t), _head_rows(k, "k", (B, T, Hk, d), t)
     _check(q_weight, "q_weight", (d,), torch.float32)
     _check(k_weight, "k_weight", (d,), torch.float32)
     R = P = 0
@@ -641,7 +676,7 @@ def _rope_inputs(q, k, q_weight, k_weight, cos_sin, positions, norm, eps, interl
         P, R = cos_sin.shape
         _check(cos_sin, "cos_sin", (P, R), torch.float32)
     _check(positions, "positions", (B, T), torch.int32)
-    return (B, T, Hq, Hk, d, _dt(q), _NORMS[norm], ctypes.c_float(eps), _some(q), lds[0], _some(k), lds[1],
+    return (B, T, Hq, Hk, d, _dt(q), _NORMS[norm], eps, _some(q), ldq, _some(k), ldk,
             _some(q_weight), _some(k_weight), R, int(bool(interleaved)), _some(cos_sin), P, _some(positions),
             int(first_position))
 
@@ -660,12 +695,12 @@ def gdr2_head_norm_rope(q, k=None, q_weight=None, k_weight=None, cos_sin=None, p
     """
     lib = load_library()
     args = _rope_inputs(q, k, q_weight, k_weight, cos_sin, positions, norm, eps, interleaved, first_position)
-    qo = q_out if q_out is not None else torch.empty(tuple(q.shape), dtype=q.dtype, device=q.device)
-    _check(qo, "q_out", tuple(q.shape), q.dtype)
+    qo = _like(q) if q_out is None else q_out
+    _check(q_out, "q_out", q.shape, q.dtype)
     ko = None
     if k is not None:
-        ko = k_out if k_out is not None else torch.empty(tuple(k.shape), dtype=q.dtype, device=q.device)
-        _check(ko, "k_out", tuple(k.shape), q.dtype)
+        ko = _like(k) if k_out is None else k_out
+        _check(k_out, "k_out", k.shape, q.dtype)
     _raise(lib, lib.gdr2_head_norm_rope(*args, _some(qo), _some(ko), _stream(stream)))
     return qo, ko
 
@@ -684,9 +719,8 @@ def gdr2_head_norm_rope_backward(q, k, dq_out, dk_out=None, q_weight=None, k_wei
         raise ValueError("k and dk_out: both or neither")
     if k is not None:
         _check(dk_out, "dk_out", tuple(k.shape), q.dtype)
-    own = lambda t: None if t is None else torch.empty(tuple(t.shape), dtype=q.dtype, device=dev)  # noqa: E731
-    f32 = lambda w: None if w is None else torch.empty((d,), dtype=torch.float32, device=dev)  # noqa: E731
-    g = {"dq": own(q), "dk": own(k), "dq_weight": f32(q_weight), "dk_weight": f32(k_weight)}
+    g = {n: None if t is None else _like(t)
+         for n, t in (("dq", q), ("dk", k), ("dq_weight", q_weight), ("dk_weight", k_weight))}
     workspace = _workspace(workspace, lib.gdr2_head_norm_rope_backward_workspace_bytes(d), dev)
     st = lib.gdr2_head_norm_rope_backward(*args, _some(dq_out), _some(dk_out), _some(g["dq"]), _some(g["dk"]),
                                           _some(g["dq_weight"]), _some(g["dk_weight"]), _some(workspace),
