@@ -10,8 +10,10 @@
 // A state before the sequence is its tokens -(W-1) .. -1, so its gradient is dx there.
 //
 // One pass over x and dy (u is formed again), one write of dx: an HBM stream of three
-// tensors. A warp walks one head over a run of tokens with the last inputs and the unfinished
-// dx rows in registers; it forms du for the W - 1 tokens after its run too, which its last dx
+// tensors. A warp walks one head over a run of tokens, four at a time: their windows are formed first, then
+// the head's two sums of all four by one butterfly that halves the eight values with each step (17 shuffles
+// instead of 40), then the gradients; the last inputs and the unfinished dx rows stay in registers, pairs of
+// channels in one 64-bit register each. It forms du for the W - 1 tokens after its run too, which its last dx
 // rows need. The weights' gradient is summed in registers over the run, then over runs and
 // sequences by a second kernel in a fixed order.
 
@@ -28,12 +30,13 @@ namespace {
 using namespace seq;
 
 constexpr int kMaxWidth = 4;
-constexpr int kRun = 64;   // tokens per warp task
-constexpr int kWarps = 8;
-constexpr int kAhead = 4;  // tokens whose loads are in flight
+constexpr int kWarps = 4;
+constexpr int kBatch = 4;  // tokens at a time: the width's ring of unfinished rows is back in place after four
+constexpr int kBlocksPerSM = 3;
+static_assert(kBatch == kMaxWidth, "a batch turns the ring once");
 
 struct ConvBwdParams {
-    int N, T, H, W, runs;
+    int N, T, H, W, run, runs;  // run: tokens per warp task (a multiple of kBatch)
     float eps;
     const void *x, *dy, *sin, *dsout;
     const float *weight;
@@ -41,139 +44,197 @@ struct ConvBwdParams {
     float *part;  // [N runs][H d][kMaxWidth]
 };
 
-template <typename T, int D, bool L2>
-__global__ void __launch_bounds__(kWarps * 32) conv_backward_kernel(ConvBwdParams p)
+// The pairs of V elements of one row, and back
+template <typename T, int V> __device__ __forceinline__ void to_pairs(const Raw<T, V> &r, f32x2 (&v)[V / 2])
 {
-    constexpr int V = D / 32;
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) v[i] = pair(r.get(2 * i), r.get(2 * i + 1));
+}
+template <typename T, int V> __device__ __forceinline__ void store_pairs(T *p, const f32x2 (&v)[V / 2])
+{
+    float o[V];
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) split(v[i], o[2 * i], o[2 * i + 1]);
+    store_vec<T, V>(p, o);
+}
+
+// Sums of eight values over a warp, in every lane.
+__device__ __forceinline__ void warp_sums(float (&v)[8], int lane)
+{
+    constexpr unsigned all = 0xffffffffu;
+#pragma unroll
+    for (int w = 4, m = 16; w >= 1; w /= 2, m /= 2) {
+        const bool up = lane & m;
+#pragma unroll
+        for (int i = 0; i < w; ++i)
+            v[i] = (up ? v[i + w] : v[i]) + __shfl_xor_sync(all, up ? v[i] : v[i + w], m);
+    }
+    float s = v[0];  // of value lane / 4
+    s += __shfl_xor_sync(all, s, 2);
+    s += __shfl_xor_sync(all, s, 1);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __shfl_sync(all, s, 4 * i);
+}
+
+template <typename T, int D, bool L2>
+__global__ void __launch_bounds__(kWarps * 32, kBlocksPerSM) conv_backward_kernel(ConvBwdParams p)
+{
+    constexpr int V = D / 32, P = V / 2, kLast = kMaxWidth - 1;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const long long task = (long long)blockIdx.x * kWarps + warp;
     if (task >= (long long)p.N * p.H * p.runs) return;
     const int h = (int)(task % p.H);
     const long long nr = task / p.H;  // sequence and run
     const int run = (int)(nr % p.runs), n = (int)(nr / p.runs);
-    const int t0 = run * kRun, t1 = min(p.T, t0 + kRun);
+    const int t0 = run * p.run, t1 = min(p.T, t0 + p.run);
     const size_t HD = (size_t)p.H * D, col = (size_t)h * D + lane * V;
     const T *x = static_cast<const T *>(p.x) + (size_t)n * p.T * HD + col;
     const T *dy = static_cast<const T *>(p.dy) + (size_t)n * p.T * HD + col;
     T *dx = static_cast<T *>(p.dx) + (size_t)n * p.T * HD + col;
     const size_t srow = (size_t)n * (p.W - 1);
 
-    float wt[kMaxWidth][V];  // right-aligned: wt[i] multiplies the input kMaxWidth - 1 - i back
+    f32x2 wt[kMaxWidth][P];  // right-aligned: wt[i] multiplies the input kLast - i back
 #pragma unroll
     for (int i = 0; i < kMaxWidth; ++i)
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
+        for (int v = 0; v < P; ++v) {
             const int j = i - (kMaxWidth - p.W);
-            wt[i][v] = j >= 0 ? __ldg(p.weight + (col + v) * p.W + j) : 0.f;
+            wt[i][v] = j >= 0 ? pair(__ldg(p.weight + (col + 2 * v) * p.W + j), __ldg(p.weight + (col + 2 * v + 1) * p.W + j))
+                              : 0;
         }
-    float xw[kMaxWidth][V], dxp[kMaxWidth][V], dw[kMaxWidth][V];
+    // xw[i]: input j0 - kLast + i of the batch at j0; dxp: ring of the unfinished rows, token j in slot (j - t0 + 3) % 4
+    f32x2 xw[kLast + kBatch][P], dxp[kMaxWidth][P], dw[kMaxWidth][P];
 #pragma unroll
     for (int i = 0; i < kMaxWidth; ++i)
 #pragma unroll
-        for (int v = 0; v < V; ++v) xw[i][v] = dxp[i][v] = dw[i][v] = 0.f;
-    // xw[i + 1] = input t0 - 3 + i: a token, a state row or zero
+        for (int v = 0; v < P; ++v) dxp[i][v] = dw[i][v] = 0;
 #pragma unroll
-    for (int i = 0; i < kMaxWidth - 1; ++i) {
-        const int t = t0 - (kMaxWidth - 1) + i, js = t + p.W - 1;
+    for (int i = 0; i < kLast; ++i) {  // a token, a state row or zero
+        const int t = t0 - kLast + i, js = t + p.W - 1;
         Raw<T, V> r;
         r.zero();
-        if (t >= 0) r.load_vec(x + (size_t)t * HD);
-        else if (p.sin && js >= 0) r.load_vec(static_cast<const T *>(p.sin) + (srow + js) * HD + col);
-#pragma unroll
-        for (int v = 0; v < V; ++v) xw[i + 1][v] = r.get(v);
+        if (t >= 0 && t < p.T) r.load_vec(x + (size_t)t * HD);
+        else if (t < 0 && p.sin && js >= 0) r.load_vec(static_cast<const T *>(p.sin) + (srow + js) * HD + col);
+        to_pairs<T, V>(r, xw[i]);
     }
-    Raw<T, V> nx[kAhead], ny[kAhead];
+    const f32x2 one = pair(1.f, 1.f), minus = pair(-1.f, -1.f);
+    // tokens past the sequence read its last one, and are cleared when they are used
+    Raw<T, V> nx[kBatch], ny[kBatch];
     auto fetch = [&](int j0) {
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-            nx[k].zero();
-            ny[k].zero();
-            if (j0 + k < p.T && j0 + k < t1 + kMaxWidth - 1) {
-                nx[k].load_vec(x + (size_t)(j0 + k) * HD);
-                ny[k].load_vec(dy + (size_t)(j0 + k) * HD);
-            }
+        for (int k = 0; k < kBatch; ++k) {
+            const size_t at = (size_t)min(j0 + k, p.T - 1) * HD;
+            nx[k].load_vec(x + at);
+            ny[k].load_vec(dy + at);
         }
     };
-    const int jend = t1 + kMaxWidth - 1, first = t0 == 0 ? -(p.W - 1) : t0;
-    fetch(t0);
-    for (int j0 = t0; j0 < jend; j0 += kAhead) {
-        Raw<T, V> cx[kAhead], cy[kAhead];
+    const int jend = t1 + kLast, first = t0 == 0 ? -(p.W - 1) : t0;
+    if (p.T > 0) fetch(t0);
+    else
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) { cx[k] = nx[k]; cy[k] = ny[k]; }
-        fetch(j0 + kAhead);
+        for (int k = 0; k < kBatch; ++k) { nx[k].zero(); ny[k].zero(); }
+    for (int j0 = t0; j0 < jend; j0 += kBatch) {
+        f32x2 g[kBatch][P];
+        if (j0 + kBatch > p.T)
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-            const int j = j0 + k;
-            if (j >= jend) break;
-            float y[V], ds[V], du[V], sg[V], u[V];
+            for (int k = 0; k < kBatch; ++k)
+                if (j0 + k >= p.T) { nx[k].zero(); ny[k].zero(); }
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
+        for (int k = 0; k < kBatch; ++k) {
+            to_pairs<T, V>(nx[k], xw[kLast + k]);
+            to_pairs<T, V>(ny[k], g[k]);
+        }
+        if (j0 + kBatch < jend && p.T > 0) fetch(j0 + kBatch);
+        f32x2 u[kBatch][P], sg[kBatch][P];
+        float sums[2 * kBatch];
 #pragma unroll
-                for (int i = 0; i < kMaxWidth - 1; ++i) xw[i][v] = xw[i + 1][v];
-                xw[kMaxWidth - 1][v] = cx[k].get(v);
-                float a = 0.f;
+        for (int k = 0; k < kBatch; ++k) {
+            f32x2 ss = 0, dot = 0;
 #pragma unroll
-                for (int i = 0; i < kMaxWidth; ++i) a = fmaf(wt[i][v], xw[i][v], a);
-                u[v] = a;
-                sg[v] = sigmoid(a);
-                y[v] = a * sg[v];
-                ds[v] = cy[k].get(v);  // zero past the sequence: its du is zero
+            for (int v = 0; v < P; ++v) {
+                f32x2 a = mul2(wt[0][v], xw[k][v]);
+#pragma unroll
+                for (int i = 1; i < kMaxWidth; ++i) a = fma2(wt[i][v], xw[k + i][v], a);
+                float lo, hi;
+                split(a, lo, hi);
+                u[k][v] = a;
+                sg[k][v] = pair(sigmoid(lo), sigmoid(hi));
+                if constexpr (L2) {
+                    const f32x2 y = mul2(a, sg[k][v]);
+                    ss = v ? fma2(y, y, ss) : mul2(y, y);
+                    dot = v ? fma2(y, g[k][v], dot) : mul2(y, g[k][v]);
+                }
             }
             if constexpr (L2) {
-                float ss = 0.f, dot = 0.f;
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    ss = fmaf(y[v], y[v], ss);
-                    dot = fmaf(y[v], ds[v], dot);
-                }
-#pragma unroll
-                for (int m = 16; m >= 1; m >>= 1) {
-                    ss += __shfl_xor_sync(0xffffffffu, ss, m);
-                    dot += __shfl_xor_sync(0xffffffffu, dot, m);
-                }
-                const float inv = j < p.T ? rsqrtf(ss + p.eps) : 0.f;
-                const float f = dot * inv * inv;
-#pragma unroll
-                for (int v = 0; v < V; ++v) ds[v] = inv * fmaf(-y[v], f, ds[v]);
+                float lo, hi;
+                split(ss, lo, hi);
+                sums[2 * k] = lo + hi;
+                split(dot, lo, hi);
+                sums[2 * k + 1] = lo + hi;
             }
+        }
+        if constexpr (L2) warp_sums(sums, lane);
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                du[v] = ds[v] * sg[v] * fmaf(u[v], 1.f - sg[v], 1.f);
-                if (j >= p.T) du[v] = 0.f;
-                if (j < t1)
-#pragma unroll
-                    for (int i = 0; i < kMaxWidth; ++i) dw[i][v] = fmaf(du[v], xw[i][v], dw[i][v]);
-#pragma unroll
-                for (int i = 0; i < kMaxWidth; ++i) dxp[i][v] = fmaf(wt[i][v], du[v], dxp[i][v]);
+        for (int k = 0; k < kBatch; ++k) {
+            const int j = j0 + k;
+            float inv = 1.f, f = 0.f;
+            if constexpr (L2) {
+                // past the sequence nothing is left of dy, but eps = 0 would leave 0 / 0
+                inv = j < p.T ? rsqrtf(sums[2 * k] + p.eps) : 0.f;
+                f = -sums[2 * k + 1] * inv * inv;
             }
-            // dxp[i] belongs to token j - 3 + i: the first is finished
-            const int t = j - (kMaxWidth - 1);
+            f32x2 du[P];
+#pragma unroll
+            for (int v = 0; v < P; ++v) {
+                const f32x2 s = sg[k][v], slope = mul2(s, fma2(u[k][v], fma2(minus, s, one), one));
+                f32x2 ds = g[k][v];
+                if constexpr (L2) ds = mul2(pair(inv, inv), fma2(mul2(u[k][v], s), pair(f, f), ds));
+                du[v] = mul2(ds, slope);
+            }
+            if (L2 && j >= p.T)
+#pragma unroll
+                for (int v = 0; v < P; ++v) du[v] = 0;
+            if (j < t1)
+#pragma unroll
+                for (int v = 0; v < P; ++v)
+#pragma unroll
+                    for (int i = 0; i < kMaxWidth; ++i) dw[i][v] = fma2(du[v], xw[k + i][v], dw[i][v]);
+#pragma unroll
+            for (int v = 0; v < P; ++v)
+#pragma unroll
+                for (int i = 0; i < kMaxWidth; ++i)
+                    dxp[(k + i) % 4][v] = i == kLast ? mul2(wt[i][v], du[v]) : fma2(wt[i][v], du[v], dxp[(k + i) % 4][v]);
+            const int t = j - kLast;  // its row is finished
             if (t >= first && t < t1) {
-                float o[V];
-#pragma unroll
-                for (int v = 0; v < V; ++v) o[v] = dxp[0][v];
                 const int js = t - (p.T - (p.W - 1));  // the final state's row that holds this input
                 if (p.dsout && js >= 0) {
                     Raw<T, V> r;
+                    f32x2 d[P];
                     r.load_vec(static_cast<const T *>(p.dsout) + (srow + js) * HD + col);
+                    to_pairs<T, V>(r, d);
 #pragma unroll
-                    for (int v = 0; v < V; ++v) o[v] += r.get(v);
+                    for (int v = 0; v < P; ++v) dxp[k][v] = add2(dxp[k][v], d[v]);
                 }
-                if (t >= 0) store_vec<T, V>(dx + (size_t)t * HD, o);
-                else if (p.dsin) store_vec<T, V>(static_cast<T *>(p.dsin) + (srow + t + p.W - 1) * HD + col, o);
-            }
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-#pragma unroll
-                for (int i = 0; i < kMaxWidth - 1; ++i) dxp[i][v] = dxp[i + 1][v];
-                dxp[kMaxWidth - 1][v] = 0.f;
+                if (t >= 0) store_pairs<T, V>(dx + (size_t)t * HD, dxp[k]);
+                else if (p.dsin) store_pairs<T, V>(static_cast<T *>(p.dsin) + (srow + t + p.W - 1) * HD + col, dxp[k]);
             }
         }
+#pragma unroll
+        for (int i = 0; i < kLast; ++i)
+#pragma unroll
+            for (int v = 0; v < P; ++v) xw[i][v] = xw[kBatch + i][v];
     }
 #pragma unroll
-    for (int v = 0; v < V; ++v)
-        *reinterpret_cast<float4 *>(p.part + ((size_t)nr * HD + col + v) * kMaxWidth) =
-            make_float4(dw[0][v], dw[1][v], dw[2][v], dw[3][v]);
+    for (int v = 0; v < P; ++v) {
+        float4 a, b;
+        split(dw[0][v], a.x, b.x);
+        split(dw[1][v], a.y, b.y);
+        split(dw[2][v], a.z, b.z);
+        split(dw[3][v], a.w, b.w);
+        float4 *o = reinterpret_cast<float4 *>(p.part + ((size_t)nr * HD + col + 2 * v) * kMaxWidth);
+        o[0] = a;
+        o[1] = b;
+    }
 }
 
 // dweight: the runs' parts, eight groups of them summed side by side and then in order.
@@ -213,20 +274,37 @@ cudaError_t launch(const ConvBwdParams &p, bool l2, float *dweight, cudaStream_t
     return cudaGetLastError();
 }
 
-int runs_of(int T) { return T > 0 ? (T + kRun - 1) / kRun : 1; }
+// Tokens per warp task: every run costs its tokens, the kLast after them and a start, and the GPU runs a number of
+// tasks at once; few sequences are cut short for latency, many run longer.
+int run_of(int N, int T, int H)
+{
+    int dev = 0, sms = 148;
+    if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    const long long slots = (long long)(sms > 0 ? sms : 148) * kBlocksPerSM * kWarps;
+    int best = 8;
+    long long least = -1;
+    for (int run = 8; run <= 256; run += run < 32 ? 4 : 16) {
+        const long long tasks = (long long)N * H * ((T + run - 1) / run);
+        const long long cost = (tasks + slots - 1) / slots * (run + 12);
+        if (least < 0 || cost < least) { least = cost; best = run; }
+    }
+    return best;
+}
+int runs_of(int T, int run) { return T > 0 ? (T + run - 1) / run : 1; }
 
 }  // namespace
 
 size_t conv_backward_workspace_bytes(int N, int T, int H, int d)
 {
-    return ((size_t)N * runs_of(T) * H * d * kMaxWidth * sizeof(float) + 255) / 256 * 256;
+    return ((size_t)N * runs_of(T, run_of(N, T, H)) * H * d * kMaxWidth * sizeof(float) + 255) / 256 * 256;
 }
 
 cudaError_t launch_conv_backward(const ConvBwdArgs &a, cudaStream_t st)
 {
     ConvBwdParams p;
     p.N = a.N; p.T = a.T; p.H = a.H; p.W = a.width;
-    p.runs = runs_of(a.T);
+    p.run = run_of(a.N, a.T, a.H);
+    p.runs = runs_of(a.T, p.run);
     p.eps = a.eps;
     p.x = a.x; p.dy = a.dy; p.sin = a.state_in; p.dsout = a.dstate_out;
     p.weight = a.weight;
