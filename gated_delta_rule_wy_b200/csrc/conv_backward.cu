@@ -10,10 +10,9 @@
 // A state before the sequence is its tokens -(W-1) .. -1, so its gradient is dx there.
 //
 // One pass over x and dy (u is formed again), one write of dx: an HBM stream of three
-// tensors. A warp walks one head over a run of tokens, four at a time: their windows are formed first, then
-// the head's two sums of all four by one butterfly that halves the eight values with each step (17 shuffles
-// instead of 40), then the gradients; the last inputs and the unfinished dx rows stay in registers, pairs of
-// channels in one 64-bit register each. It forms du for the W - 1 tokens after its run too, which its last dx
+// tensors. A warp walks one head over a run of tokens, four loads in flight. Of two tokens at a time the head's
+// two sums are taken by one butterfly that halves the four values with each step (10 shuffles instead of 20);
+// the last inputs and the unfinished dx rows stay in registers, pairs of channels in one 64-bit register each. It forms du for the W - 1 tokens after its run too, which its last dx
 // rows need. The weights' gradient is summed in registers over the run, then over runs and
 // sequences by a second kernel in a fixed order.
 
@@ -58,22 +57,22 @@ template <typename T, int V> __device__ __forceinline__ void store_pairs(T *p, c
     store_vec<T, V>(p, o);
 }
 
-// Sums of eight values over a warp, in every lane.
-__device__ __forceinline__ void warp_sums(float (&v)[8], int lane)
+// Sums of four values over a warp, in every lane.
+__device__ __forceinline__ void warp_sums(float (&v)[4], int lane)
 {
     constexpr unsigned all = 0xffffffffu;
 #pragma unroll
-    for (int w = 4, m = 16; w >= 1; w /= 2, m /= 2) {
+    for (int w = 2, m = 16; w >= 1; w /= 2, m /= 2) {
         const bool up = lane & m;
 #pragma unroll
         for (int i = 0; i < w; ++i)
             v[i] = (up ? v[i + w] : v[i]) + __shfl_xor_sync(all, up ? v[i] : v[i + w], m);
     }
-    float s = v[0];  // of value lane / 4
-    s += __shfl_xor_sync(all, s, 2);
-    s += __shfl_xor_sync(all, s, 1);
+    float s = v[0];  // of value lane / 8
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = __shfl_sync(all, s, 4 * i);
+    for (int m = 4; m >= 1; m /= 2) s += __shfl_xor_sync(all, s, m);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = __shfl_sync(all, s, 8 * i);
 }
 
 template <typename T, int D, bool L2>
@@ -133,62 +132,70 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSM) conv_backward_kerne
     else
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) { nx[k].zero(); ny[k].zero(); }
+    f32x2 u[2][P], sg[2][P], g[2][P];
+    float inv[2], f[2];
     for (int j0 = t0; j0 < jend; j0 += kBatch) {
-        f32x2 g[kBatch][P];
         if (j0 + kBatch > p.T)
 #pragma unroll
             for (int k = 0; k < kBatch; ++k)
                 if (j0 + k >= p.T) { nx[k].zero(); ny[k].zero(); }
+        Raw<T, V> gy[kBatch];
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
             to_pairs<T, V>(nx[k], xw[kLast + k]);
-            to_pairs<T, V>(ny[k], g[k]);
+            gy[k] = ny[k];
         }
         if (j0 + kBatch < jend && p.T > 0) fetch(j0 + kBatch);
-        f32x2 u[kBatch][P], sg[kBatch][P];
-        float sums[2 * kBatch];
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
-            f32x2 ss = 0, dot = 0;
+            // two tokens' sums are taken together
+            constexpr int kSub = 2;
+            if (k % kSub == 0) {
+                float sums[2 * kSub];
 #pragma unroll
-            for (int v = 0; v < P; ++v) {
-                f32x2 a = mul2(wt[0][v], xw[k][v]);
+                for (int b = 0; b < kSub; ++b) {
+                    f32x2 ss = 0, dot = 0;
+                    to_pairs<T, V>(gy[k + b], g[b]);
 #pragma unroll
-                for (int i = 1; i < kMaxWidth; ++i) a = fma2(wt[i][v], xw[k + i][v], a);
-                float lo, hi;
-                split(a, lo, hi);
-                u[k][v] = a;
-                sg[k][v] = pair(sigmoid(lo), sigmoid(hi));
+                    for (int v = 0; v < P; ++v) {
+                        f32x2 a = mul2(wt[0][v], xw[k + b][v]);
+#pragma unroll
+                        for (int i = 1; i < kMaxWidth; ++i) a = fma2(wt[i][v], xw[k + b + i][v], a);
+                        float lo, hi;
+                        split(a, lo, hi);
+                        u[b][v] = a;
+                        sg[b][v] = pair(sigmoid(lo), sigmoid(hi));
+                        if constexpr (L2) {
+                            const f32x2 y = mul2(a, sg[b][v]);
+                            ss = v ? fma2(y, y, ss) : mul2(y, y);
+                            dot = v ? fma2(y, g[b][v], dot) : mul2(y, g[b][v]);
+                        }
+                    }
+                    if constexpr (L2) {
+                        float lo, hi;
+                        split(ss, lo, hi);
+                        sums[2 * b] = lo + hi;
+                        split(dot, lo, hi);
+                        sums[2 * b + 1] = lo + hi;
+                    }
+                }
                 if constexpr (L2) {
-                    const f32x2 y = mul2(a, sg[k][v]);
-                    ss = v ? fma2(y, y, ss) : mul2(y, y);
-                    dot = v ? fma2(y, g[k][v], dot) : mul2(y, g[k][v]);
+                    warp_sums(sums, lane);
+#pragma unroll
+                    for (int b = 0; b < kSub; ++b) {
+                        // past the sequence nothing is left of dy, but eps = 0 would leave 0 / 0
+                        inv[b] = j0 + k + b < p.T ? rsqrtf(sums[2 * b] + p.eps) : 0.f;
+                        f[b] = -sums[2 * b + 1] * inv[b] * inv[b];
+                    }
                 }
             }
-            if constexpr (L2) {
-                float lo, hi;
-                split(ss, lo, hi);
-                sums[2 * k] = lo + hi;
-                split(dot, lo, hi);
-                sums[2 * k + 1] = lo + hi;
-            }
-        }
-        if constexpr (L2) warp_sums(sums, lane);
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-            const int j = j0 + k;
-            float inv = 1.f, f = 0.f;
-            if constexpr (L2) {
-                // past the sequence nothing is left of dy, but eps = 0 would leave 0 / 0
-                inv = j < p.T ? rsqrtf(sums[2 * k] + p.eps) : 0.f;
-                f = -sums[2 * k + 1] * inv * inv;
-            }
+            const int j = j0 + k, b = k % kSub;
             f32x2 du[P];
 #pragma unroll
             for (int v = 0; v < P; ++v) {
-                const f32x2 s = sg[k][v], slope = mul2(s, fma2(u[k][v], fma2(minus, s, one), one));
-                f32x2 ds = g[k][v];
-                if constexpr (L2) ds = mul2(pair(inv, inv), fma2(mul2(u[k][v], s), pair(f, f), ds));
+                const f32x2 s = sg[b][v], slope = mul2(s, fma2(u[b][v], fma2(minus, s, one), one));
+                f32x2 ds = g[b][v];
+                if constexpr (L2) ds = mul2(pair(inv[b], inv[b]), fma2(mul2(u[b][v], s), pair(f[b], f[b]), ds));
                 du[v] = mul2(ds, slope);
             }
             if (L2 && j >= p.T)
