@@ -182,7 +182,8 @@ gdr2_status head_norm_args(gdr2::HeadNormArgs &a, int B, int T, int Hq, int Hk, 
         return fail(GDR2_ERR_UNSUPPORTED, "R must be a multiple of 16, at most d (R=%d d=%d)", R, d);
     if (interleaved != 0 && interleaved != 1) return fail(GDR2_ERR_INVALID_ARG, "interleaved must be 0 or 1");
     if (P < 0 || first_position < 0) return fail(GDR2_ERR_INVALID_ARG, "negative P or first_position");
-    if (Hq > (1 << 20) || Hk > (1 << 20) || (double)B * T * (Hq + Hk) * d > 1e12)
+    // tasks of a kernel (a token's heads, four at a time) are counted in 31 bits, with room for a grid's stride
+    if (Hq > (1 << 20) || Hk > (1 << 20) || (double)B * T * (Hq + Hk + 8) > 4e9 || (double)B * T > 1e9)
         return fail(GDR2_ERR_INVALID_ARG, "problem too large");
     a = gdr2::HeadNormArgs{};
     a.tokens = (long long)B * T;

@@ -9,8 +9,12 @@
 //
 // Cosines and sines come from a table [positions][R], made by the caller in as many bits as
 // far positions need. An HBM stream: one read and one write per element (two reads and one
-// write backward). d / 8 lanes own a row of d channels, eight channels each; they walk over
-// the heads of one token, so that its angles are read once and stay in registers.
+// write backward). d / 8 lanes own a row of d channels; a lane holds both members of four pairs, so that the
+// rotation needs no shuffles, and with the weight folded into the angles a pair costs four multiplications. The lanes
+// take a few heads of one token at a time, whose sums are taken by one butterfly that halves the values with each
+// step. What the lanes need next is copied to shared memory asynchronously, two tasks ahead, by the lane
+// that uses it: with loads into registers the forward took 38 us and the backward 72 us for 4 x 4096 tokens of 16 + 2 heads
+// of 128 channels in bf16, with the copies 27 us (5.6 TB/s) and 43 us (5.3 TB/s).
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -25,11 +29,13 @@ namespace {
 using namespace seq;
 
 constexpr int kThreads = 256;
-constexpr int kMaxBlocks = 1024;  // of the backward: one partial weight gradient each
-constexpr int kHeads = 4;         // heads in flight per group
+constexpr int kMaxBlocks = 1024;  // of the backward: one partial weight gradient each, and one for the other side
+constexpr int kStages = 3;  // tasks whose copies are under way, one of them at hand
+// heads per task: what their registers allow at two blocks per SM
+constexpr int heads_per_task(bool backward) { return backward ? 2 : 4; }
 
 struct Side {
-    int H, chunks;  // heads, tasks per token
+    int H, chunks, blocks;  // heads, tasks per token, blocks
     const void *x, *dy;
     long long ld;
     const float *weight;
@@ -37,189 +43,291 @@ struct Side {
 };
 
 struct NormParams {
-    long long tokens, tasks;
-    int T, R, P, first, per;  // per: heads per task
+    int tokens, T, R, P, first;
     int norm;
-    bool interleaved;
     float eps;
     const float *cos_sin;
     const int *positions;
     Side side[2];
-    float *part;  // backward: [blocks][2][d]
+    float *part;  // backward: [blocks][d], queries' blocks first
     unsigned *status;
 };
 
-// The angles of one position for channels 8 l .. 8 l + 7 of a row: cosine and the signed sine
-// with which the partner channel enters (y_a: -sin, y_b: +sin).
-template <int D>
-__device__ __forceinline__ void load_angles(const NormParams &p, long long token, int l, float (&cs)[8], float (&sn)[8])
-{
+// A lane's eight channels as four pairs (a, b), two pairs per 64-bit register. Half-split: a and b are runs
+// of four channels, R / 2 apart (past R: two neighbouring runs). Interleaved: eight consecutive channels.
+// In shared memory they are pieces of at most 16 bytes, each kThreads pieces apart: a warp's lie side by side.
+template <typename T, bool IL> struct Row8 {
+    static constexpr int kBytes = IL || sizeof(T) == 4 ? 16 : 8;  // of a piece
+    static constexpr int kPieces = 8 * sizeof(T) / kBytes;
+    static constexpr int kSize = 8 * sizeof(T) * kThreads;        // of a row of all threads
+
+    // this thread's pieces of `row` into `to` (its first piece's place)
+    __device__ __forceinline__ static void fetch(unsigned char *to, const T *row, int ca, int cb)
+    {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) { cs[i] = 1.f; sn[i] = 0.f; }
-    if (8 * l >= p.R) return;
-    const int pos = p.positions ? __ldg(p.positions + token) : p.first + (int)(token % p.T);
-    if (pos < 0 || pos >= p.P) {  // reported; the row keeps its norm and is not turned
-        atomicOr(p.status, kStatusBadPosition);
-        return;
+        for (int i = 0; i < kPieces; ++i)
+            copy_async<kBytes>(to + i * kThreads * kBytes, row + (kPieces == 1 || i == 0 ? ca : cb));
     }
-    const float *row = p.cos_sin + (size_t)pos * p.R;
-    const int half = p.R / 2;
-    if (p.interleaved) {
-        const float4 c = __ldg(reinterpret_cast<const float4 *>(row + 4 * l));
-        const float4 s = __ldg(reinterpret_cast<const float4 *>(row + half + 4 * l));
-        const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
+    __device__ __forceinline__ static void get(const unsigned char *from, f32x2 (&a)[2], f32x2 (&b)[2])
+    {
+        float v[8];
+        if constexpr (sizeof(T) == 4) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) { cs[i] = cc[i / 2]; sn[i] = (i & 1) ? ss[i / 2] : -ss[i / 2]; }
-    } else {
-        const bool upper = 8 * l >= half;
-        const float *c = row + 8 * l - (upper ? half : 0), *s = c + half;
+            for (int i = 0; i < 2; ++i) {
+                const float4 w = *reinterpret_cast<const float4 *>(from + i * kThreads * kBytes);
+                v[4 * i] = w.x; v[4 * i + 1] = w.y; v[4 * i + 2] = w.z; v[4 * i + 3] = w.w;
+            }
+        } else {
+            Raw<T, 8> r;
+            if constexpr (IL) {
+                const uint4 w = *reinterpret_cast<const uint4 *>(from);
+                r.w[0] = w.x; r.w[1] = w.y; r.w[2] = w.z; r.w[3] = w.w;
+            } else {
+                const uint2 lo = *reinterpret_cast<const uint2 *>(from);
+                const uint2 hi = *reinterpret_cast<const uint2 *>(from + kThreads * kBytes);
+                r.w[0] = lo.x; r.w[1] = lo.y; r.w[2] = hi.x; r.w[3] = hi.y;
+            }
 #pragma unroll
-        for (int i = 0; i < 8; i += 4) {
-            const float4 a = __ldg(reinterpret_cast<const float4 *>(c + i));
-            const float4 b = __ldg(reinterpret_cast<const float4 *>(s + i));
-            const float cc[4] = {a.x, a.y, a.z, a.w}, ss[4] = {b.x, b.y, b.z, b.w};
+            for (int i = 0; i < 8; ++i) v[i] = r.get(i);
+        }
 #pragma unroll
-            for (int k = 0; k < 4; ++k) { cs[i + k] = cc[k]; sn[i + k] = upper ? ss[k] : -ss[k]; }
+        for (int i = 0; i < 2; ++i) {
+            a[i] = IL ? pair(v[4 * i], v[4 * i + 2]) : pair(v[2 * i], v[2 * i + 1]);
+            b[i] = IL ? pair(v[4 * i + 1], v[4 * i + 3]) : pair(v[4 + 2 * i], v[4 + 2 * i + 1]);
         }
     }
-}
-
-// y_i = v_i cos_i + v_partner sin_i over a row (sign = -1 turns back)
-__device__ __forceinline__ void turn(float (&v)[8], const float (&cs)[8], const float (&sn)[8], float sign,
-                                     bool interleaved, int partner)
+};
+template <typename T, bool IL>
+__device__ __forceinline__ void store_row8(T *row, int ca, int cb, const f32x2 (&a)[2], const f32x2 (&b)[2])
 {
-    float o[8];
+    float va[4], vb[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float w = interleaved ? v[i ^ 1] : __shfl_sync(0xffffffffu, v[i], partner);
-        o[i] = fmaf(v[i], cs[i], sign * sn[i] * w);
+    for (int i = 0; i < 2; ++i) {
+        split(a[i], va[2 * i], va[2 * i + 1]);
+        split(b[i], vb[2 * i], vb[2 * i + 1]);
     }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = o[i];
+    if constexpr (IL) {
+        const float v[8] = {va[0], vb[0], va[1], vb[1], va[2], vb[2], va[3], vb[3]};
+        store_vec<T, 8>(row + ca, v);
+    } else {
+        store_vec<T, 4>(row + ca, va);
+        store_vec<T, 4>(row + cb, vb);
+    }
 }
 
-template <int LANES> __device__ __forceinline__ float row_sum(float v)
+// Sums of NV values over groups of LANES lanes, in every lane.
+template <int LANES, int NV> __device__ __forceinline__ void row_sums(float (&v)[NV], int lane)
 {
+    constexpr unsigned all = 0xffffffffu;
+    int m = LANES / 2;
 #pragma unroll
-    for (int m = LANES / 2; m >= 1; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
-    return v;
+    for (int w = NV / 2; w >= 1; w /= 2, m /= 2) {
+        const bool up = lane & m;
+#pragma unroll
+        for (int i = 0; i < w; ++i)
+            v[i] = (up ? v[i + w] : v[i]) + __shfl_xor_sync(all, up ? v[i] : v[i + w], m);
+    }
+    float s = v[0];  // of value lane / (LANES / NV)
+#pragma unroll
+    for (int k = LANES / NV / 2; k >= 1; k /= 2) s += __shfl_xor_sync(all, s, k);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) v[i] = __shfl_sync(all, s, (lane & ~(LANES - 1)) + i * (LANES / NV));
 }
 
-template <typename T, int D, bool BACKWARD>
-__global__ void __launch_bounds__(kThreads) head_norm_kernel(NormParams p)
+// shared memory: per stage the task's rows (x, backward dy too), its cosines and its sines
+template <typename T, bool BACKWARD> constexpr int stage_bytes()
 {
-    constexpr int LANES = D / 8, GROUPS = kThreads / LANES;
+    return (heads_per_task(BACKWARD) * (BACKWARD ? 2 : 1) * 8 * (int)sizeof(T) + 32) * kThreads;
+}
+
+// A task: kHeads heads of one token. Its rows and angles are copied kStages - 1 tasks ahead by the lanes that use
+// them, so that nothing but a lane's own copies is ever waited for; its position is read one task before that.
+template <typename T, int D, bool BACKWARD, bool IL>
+__global__ void __launch_bounds__(kThreads, 2) head_norm_kernel(const __grid_constant__ NormParams p)
+{
+    using Row = Row8<T, IL>;
+    constexpr int LANES = D / 8, GROUPS = kThreads / LANES, PER_WARP = 32 / LANES, HB = heads_per_task(BACKWARD);
+    extern __shared__ __align__(16) unsigned char smem[];
     const int lane = threadIdx.x & 31, l = lane % LANES, grp = threadIdx.x / LANES;
-    // the lane that holds the partner channels of the half-split pairs (itself past R)
-    const int hl = p.R / 16;
-    const int partner = lane - l + (l < hl ? l + hl : l < 2 * hl ? l - hl : l);
-    float acc[2][8];
+    const bool keys = (int)blockIdx.x >= p.side[0].blocks;
+    const Side &sd = p.side[keys];
+    const int block = blockIdx.x - (keys ? p.side[0].blocks : 0);
+    const bool turns = 8 * l < p.R;  // the lane's pairs are among the first R channels
+    const int ca = IL ? 8 * l : turns ? 4 * l : p.R + 8 * (l - p.R / 8), cb = IL || !turns ? ca + 4 : ca + p.R / 2;
+    f32x2 wa[2], wb[2], acca[2], accb[2];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) acc[0][i] = acc[1][i] = 0.f;
+    for (int i = 0; i < 2; ++i) {
+        const int a0 = IL ? ca + 4 * i : ca + 2 * i, a1 = IL ? a0 + 2 : a0 + 1;
+        const int b0 = IL ? a0 + 1 : cb + 2 * i, b1 = IL ? b0 + 2 : b0 + 1;
+        wa[i] = sd.weight ? pair(__ldg(sd.weight + a0), __ldg(sd.weight + a1)) : pair(1.f, 1.f);
+        wb[i] = sd.weight ? pair(__ldg(sd.weight + b0), __ldg(sd.weight + b1)) : pair(1.f, 1.f);
+        acca[i] = accb[i] = 0;
+    }
     const float scale = p.norm == 1 ? 1.f / D : 1.f;
-    const int per_token = p.side[0].chunks + p.side[1].chunks;
-    // a warp's groups run their loops together: shuffles need every lane
-    const long long step = (long long)gridDim.x * GROUPS;
-    const long long base = (long long)blockIdx.x * GROUPS + (threadIdx.x / 32) * (32 / LANES);
-    for (long long task0 = base; task0 < p.tasks; task0 += step) {
-        const long long task = task0 + grp % (32 / LANES);
-        const bool ok = task < p.tasks;
-        const long long token = ok ? task / per_token : 0;
-        int chunk = ok ? (int)(task % per_token) : 0;
-        const int sd = chunk >= p.side[0].chunks;
-        if (sd) chunk -= p.side[0].chunks;
-        const int H = sd ? p.side[1].H : p.side[0].H;
-        const float *weight = sd ? p.side[1].weight : p.side[0].weight;
-        const T *x = static_cast<const T *>(sd ? p.side[1].x : p.side[0].x) + token * (sd ? p.side[1].ld : p.side[0].ld) +
-                     8 * l;
-        const T *dy = static_cast<const T *>(sd ? p.side[1].dy : p.side[0].dy) + (size_t)token * H * D + 8 * l;
-        T *out = static_cast<T *>(sd ? p.side[1].out : p.side[0].out) + (size_t)token * H * D + 8 * l;
-        const int h0 = chunk * p.per, h1 = ok ? min(H, h0 + p.per) : h0;
-        float cs[8], sn[8], w[8];
-        if (ok) load_angles<D>(p, token, l, cs, sn);
-        else
+    // This group's tasks are first, first + step, ...; a warp's groups run their loops together (shuffles need every
+    // lane), and a group past the last task does that one again without storing.
+    const int tasks = p.tokens * sd.chunks, step = sd.blocks * GROUPS, first = block * GROUPS + grp;
+    const int rounds = (tasks - (first - grp % PER_WARP) + step - 1) / step;
+    const int dtoken = step / sd.chunks, dchunk = step % sd.chunks;
+    struct Task {
+        int token, chunk;
+    };
+    auto advance = [&](Task &k) {
+        k.token += dtoken;
+        k.chunk += dchunk;
+        if (k.chunk >= sd.chunks) { k.chunk -= sd.chunks; ++k.token; }
+    };
+    auto position = [&](const Task &k) {
+        const int t = min(k.token, p.tokens - 1);
+        return !turns ? 0 : p.positions ? __ldg(p.positions + t) : p.first + t % p.T;
+    };
+    unsigned char *const rows = smem + threadIdx.x * Row::kBytes;
+    unsigned char *const angles = smem + kStages * HB * (BACKWARD ? 2 : 1) * Row::kSize + threadIdx.x * 16;
+    auto row_at = [&](int stage, int i) { return rows + (stage * HB * (BACKWARD ? 2 : 1) + i) * Row::kSize; };
+    auto angle_at = [&](int stage, int i) { return angles + (stage * 2 + i) * 16 * kThreads; };
+    auto fetch = [&](const Task &k, int pos, int stage) {
+        const int tok = min(k.token, p.tokens - 1);
+        const T *x = static_cast<const T *>(sd.x) + tok * sd.ld;
+        const T *dy = static_cast<const T *>(sd.dy) + (size_t)tok * sd.H * D;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) { cs[i] = 1.f; sn[i] = 0.f; }
+        for (int i = 0; i < HB; ++i) {  // heads past the last read it again
+            const int h = min(k.chunk * HB + i, sd.H - 1) * D;
+            Row::fetch(row_at(stage, i), x + h, ca, cb);
+            if constexpr (BACKWARD) Row::fetch(row_at(stage, HB + i), dy + h, ca, cb);
+        }
+        if (turns && pos >= 0 && pos < p.P) {
+            const float *row = p.cos_sin + (size_t)pos * p.R + 4 * l;
+            copy_async<16>(angle_at(stage, 0), row);
+            copy_async<16>(angle_at(stage, 1), row + p.R / 2);
+        }
+        copies_commit();
+    };
+    Task head{first / sd.chunks, first % sd.chunks}, tail = head;  // the next task to copy, and to compute
+    int pos[kStages], next = position(head);                       // of the tasks under way, and of `head`
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = weight ? __ldg(weight + 8 * l + i) : 1.f;
-        for (int hh = 0; hh < p.per; hh += kHeads) {
-            Raw<T, 8> rx[kHeads], ry[kHeads];
+    for (int i = 0; i < kStages - 1; ++i) {
+        pos[i] = next;
+        fetch(head, pos[i], i);
+        advance(head);
+        next = position(head);
+    }
+    for (int round = 0; round < rounds; round += kStages)
 #pragma unroll
-            for (int k = 0; k < kHeads; ++k) {
-                const int h = h0 + hh + k;
-                rx[k].zero();
-                if (h < h1) rx[k].load_vec(x + (size_t)h * D);
+        for (int stage = 0; stage < kStages; ++stage) {
+            if (round + stage >= rounds) break;
+            constexpr int kLast = kStages - 1;
+            const int into = (stage + kLast) % kStages;
+            pos[into] = next;
+            fetch(head, pos[into], into);  // the stage that was computed last
+            advance(head);
+            next = position(head);
+            copies_wait<kLast>();
+            const bool ok = tail.token < p.tokens;
+            const int tok = ok ? tail.token : 0, h0 = tail.chunk * HB, h1 = ok ? sd.H : 0;
+            advance(tail);
+            float4 c = make_float4(1.f, 1.f, 1.f, 1.f), s = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (turns) {
+                if (pos[stage] >= 0 && pos[stage] < p.P) {
+                    c = *reinterpret_cast<const float4 *>(angle_at(stage, 0));
+                    s = *reinterpret_cast<const float4 *>(angle_at(stage, 1));
+                } else if (ok) {  // reported; the row keeps its norm and is not turned
+                    atomicOr(p.status, kStatusBadPosition);
+                }
+            }
+            const f32x2 cs[2] = {pair(c.x, c.y), pair(c.z, c.w)}, sn[2] = {pair(s.x, s.y), pair(s.z, s.w)};
+            const f32x2 neg[2] = {pair(-s.x, -s.y), pair(-s.z, -s.w)};
+            float sums[BACKWARD ? 2 * HB : HB];
+            f32x2 a[HB][2], b[HB][2];
+            [[maybe_unused]] f32x2 ga[BACKWARD ? HB : 1][2], gb[BACKWARD ? HB : 1][2];
+#pragma unroll
+            for (int k = 0; k < HB; ++k) {
+                Row::get(row_at(stage, k), a[k], b[k]);
+                float lo, hi;
+                split(fma2(b[k][1], b[k][1], fma2(b[k][0], b[k][0], fma2(a[k][1], a[k][1], mul2(a[k][0], a[k][0])))), lo,
+                      hi);
+                sums[BACKWARD ? 2 * k : k] = lo + hi;
                 if constexpr (BACKWARD) {
-                    ry[k].zero();
-                    if (h < h1) ry[k].load_vec(dy + (size_t)h * D);
+                    f32x2 ya[2], yb[2], dot = 0;
+                    Row::get(row_at(stage, HB + k), ya, yb);
+                    if (h0 + k >= h1) ya[0] = ya[1] = yb[0] = yb[1] = 0;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {  // turned back
+                        ga[k][i] = fma2(yb[i], sn[i], mul2(ya[i], cs[i]));
+                        gb[k][i] = fma2(ya[i], neg[i], mul2(yb[i], cs[i]));
+                        const f32x2 da = mul2(ga[k][i], wa[i]);
+                        dot = i ? fma2(da, a[k][i], dot) : mul2(da, a[k][i]);
+                        dot = fma2(mul2(gb[k][i], wb[i]), b[k][i], dot);
+                    }
+                    split(dot, lo, hi);
+                    sums[2 * k + 1] = lo + hi;
+                }
+            }
+            if (p.norm) row_sums<LANES>(sums, lane);
+            T *out = static_cast<T *>(sd.out) + (size_t)tok * sd.H * D;
+            f32x2 aa[2], ab[2], ba[2], bb[2];  // y_a = a aa + b ab, y_b = a ba + b bb, but for the norm
+            if constexpr (!BACKWARD) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    aa[i] = mul2(wa[i], cs[i]);
+                    ab[i] = mul2(wb[i], neg[i]);
+                    ba[i] = mul2(wa[i], sn[i]);
+                    bb[i] = mul2(wb[i], cs[i]);
                 }
             }
 #pragma unroll
-            for (int k = 0; k < kHeads; ++k) {
-                const int h = h0 + hh + k;
-                float v[8];
-                float ss = 0.f;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) { v[i] = rx[k].get(i); ss = fmaf(v[i], v[i], ss); }
-                float inv = 1.f;
-                if (p.norm) {
-                    ss = row_sum<LANES>(ss);
-                    inv = rsqrtf(fmaf(ss, scale, p.eps));
-                }
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] *= inv;
+            for (int k = 0; k < HB; ++k) {
+                const int h = h0 + k;
+                const float inv = p.norm ? rsqrtf(fmaf(sums[BACKWARD ? 2 * k : k], scale, p.eps)) : 1.f;
+                const f32x2 inv2 = pair(inv, inv);
+                f32x2 oa[2], ob[2];
                 if constexpr (!BACKWARD) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) v[i] *= w[i];
-                    turn(v, cs, sn, 1.f, p.interleaved, partner);
-                } else {
-                    float g[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) g[i] = ry[k].get(i);
-                    turn(g, cs, sn, -1.f, p.interleaved, partner);
-                    float dot = 0.f;
-                    const bool mine = h < h1;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float dw = mine ? g[i] * v[i] : 0.f;
-                        acc[0][i] += sd ? 0.f : dw;
-                        acc[1][i] += sd ? dw : 0.f;
-                        g[i] *= w[i];
-                        dot = fmaf(g[i], v[i], dot);
+                    for (int i = 0; i < 2; ++i) {
+                        const f32x2 va = mul2(a[k][i], inv2), vb = mul2(b[k][i], inv2);
+                        oa[i] = fma2(vb, ab[i], mul2(va, aa[i]));
+                        ob[i] = fma2(va, ba[i], mul2(vb, bb[i]));
                     }
-                    if (p.norm) dot = row_sum<LANES>(dot) * scale;
-                    else dot = 0.f;
+                } else {
+                    const float f = p.norm ? -sums[2 * k + 1] * inv * scale : 0.f;
+                    const f32x2 f2 = pair(f, f);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) v[i] = inv * fmaf(-v[i], dot, g[i]);
+                    for (int i = 0; i < 2; ++i) {
+                        const f32x2 va = mul2(a[k][i], inv2), vb = mul2(b[k][i], inv2);
+                        acca[i] = fma2(ga[k][i], va, acca[i]);
+                        accb[i] = fma2(gb[k][i], vb, accb[i]);
+                        oa[i] = mul2(inv2, fma2(va, f2, mul2(ga[k][i], wa[i])));
+                        ob[i] = mul2(inv2, fma2(vb, f2, mul2(gb[k][i], wb[i])));
+                    }
                 }
-                if (h < h1) store_vec<T, 8>(out + (size_t)h * D, v);
+                if (h < h1) store_row8<T, IL>(out + (size_t)h * D, ca, cb, oa, ob);
             }
         }
-    }
+    copies_wait<0>();
     if constexpr (BACKWARD) {
-        __shared__ float sm[GROUPS][2][D];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            sm[grp][0][8 * l + i] = acc[0][i];
-            sm[grp][1][8 * l + i] = acc[1][i];
-        }
         __syncthreads();
-        for (int i = threadIdx.x; i < 2 * D; i += kThreads) {
+        float *sm = reinterpret_cast<float *>(smem);  // [GROUPS][D]
+        store_row8<float, IL>(sm + grp * D, ca, cb, acca, accb);
+        __syncthreads();
+        for (int i = threadIdx.x; i < D; i += kThreads) {
             float s = 0.f;
-            for (int k = 0; k < GROUPS; ++k) s += sm[k][i / D][i % D];
-            p.part[(size_t)blockIdx.x * 2 * D + i] = s;
+            for (int k = 0; k < GROUPS; ++k) s += sm[k * D + i];
+            p.part[(size_t)blockIdx.x * D + i] = s;
         }
     }
 }
 
-// dweight of both sides: one warp per value over the blocks' parts, always the same order.
-__global__ void __launch_bounds__(256) head_norm_dweight_kernel(const float *part, int blocks, int d, float *dq, float *dk)
+// dweight of both sides: one warp per value over its blocks' parts, always the same order.
+__global__ void __launch_bounds__(256) head_norm_dweight_kernel(const float *part, int qblocks, int kblocks, int d,
+                                                                float *dq, float *dk)
 {
     const int lane = threadIdx.x & 31, i = blockIdx.x * 8 + (threadIdx.x >> 5);
     if (i >= 2 * d) return;
+    const float *src = part + (i < d ? i : (size_t)qblocks * d + i - d);
+    const int blocks = i < d ? qblocks : kblocks;
     float s = 0.f;
-    for (int b = lane; b < blocks; b += 32) s += part[(size_t)b * 2 * d + i];
-    s = row_sum<32>(s);
+    for (int b = lane; b < blocks; b += 32) s += src[(size_t)b * d];
+#pragma unroll
+    for (int m = 16; m >= 1; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
     float *out = i < d ? dq : dk;
     if (lane == 0 && out) out[i % d] = s;
 }
@@ -234,37 +342,39 @@ int sm_count()
 template <typename T, int D, bool BACKWARD>
 cudaError_t launch(const HeadNormArgs &a, cudaStream_t st)
 {
-    constexpr int GROUPS = kThreads / (D / 8);
+    constexpr int GROUPS = kThreads / (D / 8), HB = heads_per_task(BACKWARD);
     const int sms = sm_count();
     NormParams p;
-    // heads per task: all of a side where that still fills the GPU, else few, for latency
-    const int most = a.side[0].H > a.side[1].H ? a.side[0].H : a.side[1].H;
-    p.per = kHeads;
-    while (p.per < most && a.tokens * ((most + 2 * p.per - 1) / (2 * p.per)) >= 8LL * sms * GROUPS) p.per *= 2;
-    p.tokens = a.tokens;
+    p.tokens = (int)a.tokens;
     p.T = a.T > 0 ? a.T : 1;
     p.R = a.R; p.P = a.P; p.first = a.first;
-    p.norm = a.norm; p.interleaved = a.interleaved; p.eps = a.eps;
+    p.norm = a.norm; p.eps = a.eps;
     p.cos_sin = a.cos_sin; p.positions = a.positions;
     p.status = a.status;
     p.part = static_cast<float *>(a.workspace);
-    int per_token = 0;
+    const long long chunks[2] = {(a.side[0].H + HB - 1) / HB, (a.side[1].H + HB - 1) / HB};  // tasks per token
+    const long long cap = 2LL * sms < kMaxBlocks ? 2LL * sms : kMaxBlocks, all = chunks[0] + chunks[1];
     for (int s = 0; s < 2; ++s) {
         const HeadNormSide &h = a.side[s];
-        p.side[s] = Side{h.H, (h.H + p.per - 1) / p.per, h.x, h.dy, h.ld, h.weight, h.out};
-        per_token += p.side[s].chunks;
+        const long long want = (a.tokens * chunks[s] + GROUPS - 1) / GROUPS;
+        long long share = all ? (cap * chunks[s] + all / 2) / all : 0;  // of the resident blocks, as of the work
+        if (share < 1) share = 1;
+        p.side[s] = Side{h.H, (int)(chunks[s] ? chunks[s] : 1), (int)(want < share ? want : share), h.x, h.dy, h.ld, h.weight,
+                         h.out};
     }
-    p.tasks = a.tokens * per_token;
-    const long long want = (p.tasks + GROUPS - 1) / GROUPS;
-    const long long cap = BACKWARD ? (kMaxBlocks < 4LL * sms ? kMaxBlocks : 4LL * sms) : 16LL * sms;
-    const int blocks = (int)(want < cap ? want : cap);
+    const int blocks = p.side[0].blocks + p.side[1].blocks;
     if (blocks > 0) {
-        head_norm_kernel<T, D, BACKWARD><<<blocks, kThreads, 0, st>>>(p);
-        const cudaError_t e = cudaGetLastError();
+        constexpr int smem = kStages * stage_bytes<T, BACKWARD>();
+        auto *kern = a.interleaved ? head_norm_kernel<T, D, BACKWARD, true> : head_norm_kernel<T, D, BACKWARD, false>;
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        kern<<<blocks, kThreads, smem, st>>>(p);
+        e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
     if (BACKWARD && (a.side[0].dweight || a.side[1].dweight)) {
-        head_norm_dweight_kernel<<<(2 * D + 7) / 8, 256, 0, st>>>(p.part, blocks, D, a.side[0].dweight, a.side[1].dweight);
+        head_norm_dweight_kernel<<<(2 * D + 7) / 8, 256, 0, st>>>(p.part, p.side[0].blocks, p.side[1].blocks, D,
+                                                                 a.side[0].dweight, a.side[1].dweight);
         return cudaGetLastError();
     }
     return cudaSuccess;
@@ -283,7 +393,7 @@ template <bool BACKWARD> cudaError_t dispatch(const HeadNormArgs &a, cudaStream_
 
 }  // namespace
 
-size_t head_norm_backward_workspace_bytes(int d) { return (size_t)kMaxBlocks * 2 * d * sizeof(float); }
+size_t head_norm_backward_workspace_bytes(int d) { return (size_t)(kMaxBlocks + 2) * d * sizeof(float); }
 cudaError_t launch_head_norm_rope(const HeadNormArgs &a, cudaStream_t st) { return dispatch<false>(a, st); }
 cudaError_t launch_head_norm_rope_backward(const HeadNormArgs &a, cudaStream_t st) { return dispatch<true>(a, st); }
 

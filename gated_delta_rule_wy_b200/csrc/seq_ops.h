@@ -131,6 +131,19 @@ template <typename T> __device__ __forceinline__ float bits_value(uint32_t b)
     return __uint_as_float(sizeof(T) == 2 ? b << 16 : b);
 }
 
+// Asynchronous copies to shared memory, BYTES (4, 8 or 16) each, and their groups.
+template <int BYTES> __device__ __forceinline__ void copy_async(void *dst, const void *src)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"((unsigned)__cvta_generic_to_shared(dst)), "l"(src),
+                 "n"(BYTES)
+                 : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT> __device__ __forceinline__ void copies_wait()  // until at most LEFT groups are under way
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
+}
+
 constexpr float kLog2e = 1.4426950408889634f;
 
 // 2^x on the special-function unit (relative error 2^-22; 0 below the normal range)
