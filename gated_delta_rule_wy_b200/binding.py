@@ -485,8 +485,8 @@ def gdr2_short_conv_silu_backward(x, weight, dy, state=None, dstate_out=None, *,
 
 
 def _some(t):
-    """The data pointer, or NULL for None and for a tensor without elements."""
-    return None if t is None or t.numel() == 0 else t.data_ptr()
+    """The data pointer; NULL for None (and for a tensor without elements, whose pointer is 0)."""
+    return None if t is None else t.data_ptr()
 
 
 def _nbytes(t):

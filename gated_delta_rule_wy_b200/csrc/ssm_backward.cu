@@ -510,37 +510,42 @@ __global__ void __launch_bounds__(BwdShape<N>::kBlock, BwdShape<N>::kBlocks) ssm
     }
 }
 
-// dB and dC: the blocks' sums, in the order of the blocks. rows = B T; one thread per value.
-template <typename T>
-__global__ void ssm_reduce_bc_kernel(const float *pBC, long long rows, int N, int ncb, T *dBm, T *dCm)
-{
-    const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x, n = rows * 2 * N;
-    if (i >= n) return;
-    float s = 0.f;
-#pragma unroll 8
-    for (int b = 0; b < ncb; ++b) s += pBC[b * n + i];
-    const long long row = i / (2 * N);
-    const int j = (int)(i % (2 * N));
-    if (j < N) store_one(dBm + row * N + j, s);
-    else store_one(dCm + row * N + j - N, s);
-}
+struct ReduceParams {
+    const float *pBC, *pA, *pD;
+    long long rows;             // B T
+    int N, D, ncb, parts;       // parts: segments and batch entries
+    unsigned bc_blocks;         // the first blocks: dB and dC
+    float *dA, *dD, *dbias;
+};
 
-// dA, dDskip and dbias: the sums over segments and batch entries, in their order.
-__global__ void ssm_reduce_param_kernel(const float *pA, const float *pD, int parts, int D, int N, float *dA, float *dD,
-                                        float *dbias)
+// One thread per value, always in the same order: dB and dC over the blocks' channels, then dA, dDskip and dbias
+// over segments and batch entries.
+template <typename T> __global__ void __launch_bounds__(256) ssm_reduce_kernel(ReduceParams p, T *dBm, T *dCm)
 {
-    const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x, nA = (long long)D * N;
+    if (blockIdx.x < p.bc_blocks) {
+        const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x, n = p.rows * 2 * p.N;
+        if (i >= n) return;
+        float s = 0.f;
+#pragma unroll 8
+        for (int b = 0; b < p.ncb; ++b) s += p.pBC[b * n + i];
+        const long long row = i / (2 * p.N);
+        const int j = (int)(i % (2 * p.N));
+        if (j < p.N) store_one(dBm + row * p.N + j, s);
+        else store_one(dCm + row * p.N + j - p.N, s);
+        return;
+    }
+    const long long i = (long long)(blockIdx.x - p.bc_blocks) * blockDim.x + threadIdx.x, nA = (long long)p.D * p.N;
     if (i < nA) {
         float s = 0.f;
-        for (int k = 0; k < parts; ++k) s += pA[k * nA + i];
-        dA[i] = s;
-    } else if (i < nA + 2LL * D) {
+        for (int k = 0; k < p.parts; ++k) s += p.pA[k * nA + i];
+        p.dA[i] = s;
+    } else if (i < nA + 2LL * p.D) {
         const long long j = i - nA;  // dDskip, then dbias
-        float *out = j < D ? dD : dbias;
+        float *out = j < p.D ? p.dD : p.dbias;
         if (!out) return;
         float s = 0.f;
-        for (int k = 0; k < parts; ++k) s += pD[k * 2LL * D + j];
-        out[j < D ? j : j - D] = s;
+        for (int k = 0; k < p.parts; ++k) s += p.pD[k * 2LL * p.D + j];
+        out[j < p.D ? j : j - p.D] = s;
     }
 }
 
@@ -571,15 +576,14 @@ cudaError_t launch_bwd(const SsmArgs &a, const SsmGrads &g, const BwdParams &p, 
     const int rest = p.nseg > 1 ? p.nseg - 1 : 1;
     e = vec ? run(ssm_backward_kernel<T, N, true, false>, rest) : run(ssm_backward_kernel<T, N, false, false>, rest);
     if (e != cudaSuccess) return e;
-    const long long rows = (long long)a.B * a.T, nbc = rows * 2 * N;
-    ssm_reduce_bc_kernel<T><<<(unsigned)((nbc + 255) / 256), 256, 0, st>>>(p.pBC, rows, N, p.ncb,
-                                                                          static_cast<T *>(g.dBm),
-                                                                          static_cast<T *>(g.dCm));
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    const long long np = (long long)a.D * (N + 2);
-    ssm_reduce_param_kernel<<<(unsigned)((np + 255) / 256), 256, 0, st>>>(p.pA, p.pD, a.B * p.nseg, a.D, N, g.dA, g.dD,
-                                                                         g.dbias);
+    ReduceParams r;
+    r.pBC = p.pBC; r.pA = p.pA; r.pD = p.pD;
+    r.rows = (long long)a.B * a.T;
+    r.N = N; r.D = a.D; r.ncb = p.ncb; r.parts = a.B * p.nseg;
+    r.bc_blocks = (unsigned)((r.rows * 2 * N + 255) / 256);
+    r.dA = g.dA; r.dD = g.dD; r.dbias = g.dbias;
+    const unsigned more = (unsigned)(((long long)a.D * (N + 2) + 255) / 256);
+    ssm_reduce_kernel<T><<<r.bc_blocks + more, 256, 0, st>>>(r, static_cast<T *>(g.dBm), static_cast<T *>(g.dCm));
     return cudaGetLastError();
 }
 
