@@ -421,7 +421,8 @@ __global__ void __launch_bounds__(kThreads) ssm_step_kernel(StepParams p)
         rdt[o] = load_bits(static_cast<const T *>(p.dt) + seq * p.lddt + c);
         rz[o] = p.z ? load_bits(static_cast<const T *>(p.z) + seq * p.ldz + c) : 0u;
     }
-    const float4 a = __ldg(reinterpret_cast<const float4 *>(p.A + (size_t)c * N + 4 * q));
+    float4 a = __ldg(reinterpret_cast<const float4 *>(p.A + (size_t)c * N + 4 * q));
+    a.x *= kLog2e; a.y *= kLog2e; a.z *= kLog2e; a.w *= kLog2e;
     const float bias = p.bias ? __ldg(p.bias + c) : 0.f, skip = p.Dskip ? __ldg(p.Dskip + c) : 0.f;
     float d[OWN], x[OWN];
 #pragma unroll
@@ -435,11 +436,11 @@ __global__ void __launch_bounds__(kThreads) ssm_step_kernel(StepParams p)
     for (int s = 0; s < SEQS; ++s) {
         const int from = lane - q + s % DEAL;
         const float ds = __shfl_sync(all, d[s / DEAL], from), xs = __shfl_sync(all, x[s / DEAL], from);
-        const float u = ds * xs, d2 = ds * kLog2e;
-        h[s].x = fmaf(ex2(d2 * a.x), h[s].x, u * bits_value<T>(rb[s][0]));
-        h[s].y = fmaf(ex2(d2 * a.y), h[s].y, u * bits_value<T>(rb[s][1]));
-        h[s].z = fmaf(ex2(d2 * a.z), h[s].z, u * bits_value<T>(rb[s][2]));
-        h[s].w = fmaf(ex2(d2 * a.w), h[s].w, u * bits_value<T>(rb[s][3]));
+        const float u = ds * xs;
+        h[s].x = fmaf(ex2(ds * a.x), h[s].x, u * bits_value<T>(rb[s][0]));
+        h[s].y = fmaf(ex2(ds * a.y), h[s].y, u * bits_value<T>(rb[s][1]));
+        h[s].z = fmaf(ex2(ds * a.z), h[s].z, u * bits_value<T>(rb[s][2]));
+        h[s].w = fmaf(ex2(ds * a.w), h[s].w, u * bits_value<T>(rb[s][3]));
         if (live && s0 + s < p.B)
             *reinterpret_cast<float4 *>(p.S + ((size_t)(s0 + s) * p.D + c) * N + 4 * q) = h[s];
         part[s] = fmaf(bits_value<T>(rc[s][0]), h[s].x, bits_value<T>(rc[s][1]) * h[s].y) +

@@ -178,3 +178,7 @@ def test_row_strides_of_views():
                          (base[:, :1].expand(2, 6, 40), (2, 6), 40)):
         with pytest.raises(ValueError):
             rows(bad, lead, w)
+
+
+def test_norm_and_rotation_refuse_what_their_counters_cannot_hold(lib):
+    assert rope(lib, B=40000, T=40000, n=40000) == b.GDR2_ERR_INVALID_ARG and b"large" in lib.gdr2_last_error()
