@@ -130,7 +130,7 @@ __device__ __forceinline__ void walk_segment(const BwdParams &p, int g, float *s
             *reinterpret_cast<float4 *>(base + (index * p.D + c) * N + 4 * (warp * R + r)) =
                 make_float4(w[0], w[1], w[2], w[3]);
         };
-        auto decay = [&](float d, int r, int k) { return pair(ex2(d * A2[r][2 * k]), ex2(d * A2[r][2 * k + 1])); };
+        auto decay = [&](float d, int r, int k) { return pair(decay2(d, A2[r][2 * k]), decay2(d, A2[r][2 * k + 1])); };
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             e[r][0] = e[r][1] = A[r][0] = A[r][1] = dA[r][0] = dA[r][1] = 0;
@@ -177,7 +177,7 @@ __device__ __forceinline__ void walk_segment(const BwdParams &p, int g, float *s
         fetch_saved(nt - 1);
         for (int it = nt - 1; it >= 0; --it) {
             __syncthreads();
-            const int buf = it & 1, t0 = tbeg + it * kTile;
+            const int buf = it & 1;
             auto du_at = [&](int t) { return *reinterpret_cast<const float2 *>(sdu + (buf * kTile + t) * S::kDuRow); };
             auto g_at = [&](int t) { return sg[(buf * kTile + t) * S::kGRow]; };
             auto bc_at = [&](int t, int which, int r, f32x2 (&v)[2]) {
@@ -204,6 +204,7 @@ __device__ __forceinline__ void walk_segment(const BwdParams &p, int g, float *s
                 fetch_saved(it - 1);
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
+                    f32x2 sA[2] = {0, 0};  // the tile's part of dA: sums of sums round less than one long one
                     // the compiler reads shared memory anew behind this: it would keep every token's decays for
                     // the walk back instead of forming them again, in 64 registers
                     auto forget = [] { asm volatile("" ::: "memory"); };
@@ -252,7 +253,7 @@ __device__ __forceinline__ void walk_segment(const BwdParams &p, int g, float *s
                                 split(mul2(gg, h[i][k]), vc[2 * k], vc[2 * k + 1]);
                                 e[r][k] = mul2(decay(now.du.x, r, k), dh);
                                 const f32x2 m = mul2(e[r][k], prev);
-                                dA[r][k] = fma2(dd, m, dA[r][k]);
+                                sA[k] = fma2(dd, m, sA[k]);
                                 sdx = k ? fma2(now.b[k], dh, sdx) : mul2(now.b[k], dh);
                                 sdd = k ? fma2(A[r][k], m, sdd) : mul2(A[r][k], m);
                                 sy = k ? fma2(now.c[k], h[i][k], sy) : mul2(now.c[k], h[i][k]);
@@ -277,6 +278,8 @@ __device__ __forceinline__ void walk_segment(const BwdParams &p, int g, float *s
                     forget();
                     walk(std::integral_constant<int, kHalf>{}, middle);
                     walk(std::integral_constant<int, 0>{}, first[r]);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) dA[r][k] = add2(dA[r][k], sA[k]);
                 }
             }
         }
@@ -354,7 +357,7 @@ __device__ __forceinline__ void walk_segment(const BwdParams &p, int g, float *s
         }
         if (p.softplus)
 #pragma unroll
-            for (int i = 0; i < E; ++i) { sg[i] = sigmoid(d[i]); d[i] = softplus(d[i]); }
+            for (int i = 0; i < E; ++i) { sg[i] = softplus_slope(d[i]); d[i] = softplus(d[i]); }
         if (z)
 #pragma unroll
             for (int i = 0; i < E; ++i) {

@@ -113,7 +113,7 @@ __device__ __forceinline__ void scan_segment(const ScanParams &p, int g, float *
             split(h[1], a.z, a.w);
             *reinterpret_cast<float4 *>(base + (index * p.D + c) * N + 4 * q) = a;
         };
-        auto decay = [&](float d, int k) { return pair(ex2(d * A2[2 * k]), ex2(d * A2[2 * k + 1])); };
+        auto decay = [&](float d, int k) { return pair(decay2(d, A2[2 * k]), decay2(d, A2[2 * k + 1])); };
         auto initial = [&](int s) {  // the state before sequence s
             if (p.S0 && live) load_state(p.S0, s, h);
             else h[0] = h[1] = 0;
@@ -437,10 +437,10 @@ __global__ void __launch_bounds__(kThreads) ssm_step_kernel(StepParams p)
         const int from = lane - q + s % DEAL;
         const float ds = __shfl_sync(all, d[s / DEAL], from), xs = __shfl_sync(all, x[s / DEAL], from);
         const float u = ds * xs;
-        h[s].x = fmaf(ex2(ds * a.x), h[s].x, u * bits_value<T>(rb[s][0]));
-        h[s].y = fmaf(ex2(ds * a.y), h[s].y, u * bits_value<T>(rb[s][1]));
-        h[s].z = fmaf(ex2(ds * a.z), h[s].z, u * bits_value<T>(rb[s][2]));
-        h[s].w = fmaf(ex2(ds * a.w), h[s].w, u * bits_value<T>(rb[s][3]));
+        h[s].x = fmaf(decay2(ds, a.x), h[s].x, u * bits_value<T>(rb[s][0]));
+        h[s].y = fmaf(decay2(ds, a.y), h[s].y, u * bits_value<T>(rb[s][1]));
+        h[s].z = fmaf(decay2(ds, a.z), h[s].z, u * bits_value<T>(rb[s][2]));
+        h[s].w = fmaf(decay2(ds, a.w), h[s].w, u * bits_value<T>(rb[s][3]));
         if (live && s0 + s < p.B)
             *reinterpret_cast<float4 *>(p.S + ((size_t)(s0 + s) * p.D + c) * N + 4 * q) = h[s];
         part[s] = fmaf(bits_value<T>(rc[s][0]), h[s].x, bits_value<T>(rc[s][1]) * h[s].y) +

@@ -63,6 +63,20 @@ def test_gates_and_slopes_over_their_whole_range():
     assert np.all(np.abs(np64(h["ddt"][0, 0]) - s) <= limit * s + 1e-37)
 
 
+def test_a_step_of_zero_leaves_the_state():
+    """Bit for bit: the tokens that fill up a tile are such steps."""
+    v = cuda(make((2, 41), 50, 16, torch.float32, 30, states=2))
+    v.update(dt=torch.zeros_like(v["dt"]), dt_bias=None)
+    y, S_T, _ = gdr2_ssm_scan(**v, softplus=False)
+    d = {k: t[:, 0].contiguous() if k in ("x", "dt", "Bm", "Cm", "z") else t for k, t in v.items()}
+    S = d.pop("S0").clone()
+    gdr2_ssm_step(**d, S=S, softplus=False)
+    dS = torch.randn((2, 50, 16), generator=torch.Generator().manual_seed(9))
+    g = backward({k: None if t is None else t.cpu() for k, t in v.items()}, torch.zeros((2, 41, 50)), dS, softplus=False)
+    gdr2_sync_status()
+    assert torch.equal(S_T, v["S0"]) and torch.equal(S, v["S0"]) and torch.equal(g["dS0"].cpu(), dS)
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("N,C", [(16, 33), (8, 70), (32, 40)])
 def test_long_sequences_in_many_segments(dtype, N, C):
