@@ -20,6 +20,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "gdr2_launch.h"
 #include "seq_ops.h"
 
@@ -31,7 +33,9 @@ using namespace seq;
 constexpr int kMaxWidth = 4;
 constexpr int kWarps = 4;
 constexpr int kBatch = 4;  // tokens at a time: the width's ring of unfinished rows is back in place after four
-constexpr int kBlocksPerSM = 3;
+// Blocks per SM that the registers are held to. (bf16, 4 x 4096 tokens of 16 heads: d = 128 with the norm 68 us at three, 92
+// at four with spills, 78 at two; without it 55 at four, 63 at three; d = 64 with the norm 44 at four, 50 at three.)
+template <typename T, int D, bool L2> constexpr int blocks_per_sm() { return D == 64 || (sizeof(T) == 2 && !L2) ? 4 : 3; }
 static_assert(kBatch == kMaxWidth, "a batch turns the ring once");
 
 struct ConvBwdParams {
@@ -76,7 +80,7 @@ __device__ __forceinline__ void warp_sums(float (&v)[4], int lane)
 }
 
 template <typename T, int D, bool L2>
-__global__ void __launch_bounds__(kWarps * 32, kBlocksPerSM) conv_backward_kernel(ConvBwdParams p)
+__global__ void __launch_bounds__(kWarps * 32, blocks_per_sm<T, D, L2>()) conv_backward_kernel(ConvBwdParams p)
 {
     constexpr int V = D / 32, P = V / 2, kLast = kMaxWidth - 1;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -120,6 +124,15 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSM) conv_backward_kerne
     // tokens past the sequence read its last one, and are cleared when they are used
     Raw<T, V> nx[kBatch], ny[kBatch];
     auto fetch = [&](int j0) {
+        if (j0 + kBatch <= p.T) {
+            const T *px = x + (size_t)j0 * HD, *py = dy + (size_t)j0 * HD;
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k, px += HD, py += HD) {
+                nx[k].load_vec(px);
+                ny[k].load_vec(py);
+            }
+            return;
+        }
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
             const size_t at = (size_t)min(j0 + k, p.T - 1) * HD;
@@ -134,8 +147,12 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSM) conv_backward_kerne
         for (int k = 0; k < kBatch; ++k) { nx[k].zero(); ny[k].zero(); }
     f32x2 u[2][P], sg[2][P], g[2][P];
     float inv[2], f[2];
-    for (int j0 = t0; j0 < jend; j0 += kBatch) {
-        if (j0 + kBatch > p.T)
+    // INNER: every token of the batch is one of the run's, and every row it finishes is one of the run's tokens
+    // that no final state holds: none of the tests below
+    auto batch = [&](int j0, auto inner) {
+        constexpr bool INNER = decltype(inner)::value;
+        T *out = dx + (size_t)(INNER ? j0 - kLast : 0) * HD;
+        if (!INNER && j0 + kBatch > p.T)
 #pragma unroll
             for (int k = 0; k < kBatch; ++k)
                 if (j0 + k >= p.T) { nx[k].zero(); ny[k].zero(); }
@@ -151,10 +168,10 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSM) conv_backward_kerne
             // two tokens' sums are taken together
             constexpr int kSub = 2;
             if (k % kSub == 0) {
-                float sums[2 * kSub];
+                [[maybe_unused]] float sums[2 * kSub];
 #pragma unroll
                 for (int b = 0; b < kSub; ++b) {
-                    f32x2 ss = 0, dot = 0;
+                    [[maybe_unused]] f32x2 ss = 0, dot = 0;
                     to_pairs<T, V>(gy[k + b], g[b]);
 #pragma unroll
                     for (int v = 0; v < P; ++v) {
@@ -184,7 +201,7 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSM) conv_backward_kerne
 #pragma unroll
                     for (int b = 0; b < kSub; ++b) {
                         // past the sequence nothing is left of dy, but eps = 0 would leave 0 / 0
-                        inv[b] = j0 + k + b < p.T ? rsqrtf(sums[2 * b] + p.eps) : 0.f;
+                        inv[b] = INNER || j0 + k + b < p.T ? rsqrtf(sums[2 * b] + p.eps) : 0.f;
                         f[b] = -sums[2 * b + 1] * inv[b] * inv[b];
                     }
                 }
@@ -198,10 +215,10 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSM) conv_backward_kerne
                 if constexpr (L2) ds = mul2(pair(inv[b], inv[b]), fma2(mul2(u[b][v], s), pair(f[b], f[b]), ds));
                 du[v] = mul2(ds, slope);
             }
-            if (L2 && j >= p.T)
+            if (!INNER && L2 && j >= p.T)
 #pragma unroll
                 for (int v = 0; v < P; ++v) du[v] = 0;
-            if (j < t1)
+            if (INNER || j < t1)
 #pragma unroll
                 for (int v = 0; v < P; ++v)
 #pragma unroll
@@ -212,7 +229,10 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSM) conv_backward_kerne
                 for (int i = 0; i < kMaxWidth; ++i)
                     dxp[(k + i) % 4][v] = i == kLast ? mul2(wt[i][v], du[v]) : fma2(wt[i][v], du[v], dxp[(k + i) % 4][v]);
             const int t = j - kLast;  // its row is finished
-            if (t >= first && t < t1) {
+            if constexpr (INNER) {
+                store_pairs<T, V>(out, dxp[k]);
+                out += HD;
+            } else if (t >= first && t < t1) {
                 const int js = t - (p.T - (p.W - 1));  // the final state's row that holds this input
                 if (p.dsout && js >= 0) {
                     Raw<T, V> r;
@@ -230,6 +250,10 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSM) conv_backward_kerne
         for (int i = 0; i < kLast; ++i)
 #pragma unroll
             for (int v = 0; v < P; ++v) xw[i][v] = xw[kBatch + i][v];
+    };
+    for (int j0 = t0; j0 < jend; j0 += kBatch) {
+        if (j0 >= t0 + kLast && j0 + kBatch <= t1) batch(j0, std::true_type{});
+        else batch(j0, std::false_type{});
     }
 #pragma unroll
     for (int v = 0; v < P; ++v) {
@@ -283,11 +307,11 @@ cudaError_t launch(const ConvBwdParams &p, bool l2, float *dweight, cudaStream_t
 
 // Tokens per warp task: every run costs its tokens, the kLast after them and a start, and the GPU runs a number of
 // tasks at once; few sequences are cut short for latency, many run longer.
-int run_of(int N, int T, int H)
+int run_of(int N, int T, int H, int d)
 {
     int dev = 0, sms = 148;
     if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    const long long slots = (long long)(sms > 0 ? sms : 148) * kBlocksPerSM * kWarps;
+    const long long slots = (long long)(sms > 0 ? sms : 148) * (d == 64 ? 4 : 3) * kWarps;
     int best = 8;
     long long least = -1;
     for (int run = 8; run <= 256; run += run < 32 ? 4 : 16) {
@@ -303,14 +327,14 @@ int runs_of(int T, int run) { return T > 0 ? (T + run - 1) / run : 1; }
 
 size_t conv_backward_workspace_bytes(int N, int T, int H, int d)
 {
-    return ((size_t)N * runs_of(T, run_of(N, T, H)) * H * d * kMaxWidth * sizeof(float) + 255) / 256 * 256;
+    return ((size_t)N * runs_of(T, run_of(N, T, H, d)) * H * d * kMaxWidth * sizeof(float) + 255) / 256 * 256;
 }
 
 cudaError_t launch_conv_backward(const ConvBwdArgs &a, cudaStream_t st)
 {
     ConvBwdParams p;
     p.N = a.N; p.T = a.T; p.H = a.H; p.W = a.width;
-    p.run = run_of(a.N, a.T, a.H);
+    p.run = run_of(a.N, a.T, a.H, a.d);
     p.runs = runs_of(a.T, p.run);
     p.eps = a.eps;
     p.x = a.x; p.dy = a.dy; p.sin = a.state_in; p.dsout = a.dstate_out;
