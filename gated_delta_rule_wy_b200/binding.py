@@ -154,7 +154,8 @@ def _one_device(fn):
     The library launches on the current CUDA device and stream, so tensors on another
     device would reach kernels as foreign pointers: the call is made under that device
     (its current stream unless one is given), after checking that every tensor argument
-    and the stream share it.
+    and the stream share it. A given stream is the current one during the call, so that outputs and
+    scratch are allocated in its order.
     """
     @functools.wraps(fn)
     def call(*args, **kwargs):
@@ -173,6 +174,9 @@ def _one_device(fn):
         stream = kwargs.get("stream")
         if stream is not None and stream.device != dev:
             raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}: one CUDA device per call")
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return fn(*args, **kwargs)
         if torch.cuda.current_device() == dev.index:
             return fn(*args, **kwargs)
         with torch.cuda.device(dev):

@@ -34,8 +34,8 @@ constexpr int kMaxWidth = 4;
 constexpr int kWarps = 4;
 constexpr int kBatch = 4;  // tokens at a time: the width's ring of unfinished rows is back in place after four
 // Blocks per SM that the registers are held to. (bf16, 4 x 4096 tokens of 16 heads: d = 128 with the norm 68 us at three, 92
-// at four with spills, 78 at two; without it 55 at four, 63 at three; d = 64 with the norm 44 at four, 50 at three.)
-template <typename T, int D, bool L2> constexpr int blocks_per_sm() { return D == 64 || (sizeof(T) == 2 && !L2) ? 4 : 3; }
+// at four with spills, 78 at two; without it 63 at three, 55 to 64 at four; d = 64 with the norm 44 at four, 50 at three.)
+template <int D> constexpr int blocks_per_sm() { return D == 64 ? 4 : 3; }
 static_assert(kBatch == kMaxWidth, "a batch turns the ring once");
 
 struct ConvBwdParams {
@@ -79,8 +79,10 @@ __device__ __forceinline__ void warp_sums(float (&v)[4], int lane)
     for (int i = 0; i < 4; ++i) v[i] = __shfl_sync(all, s, 8 * i);
 }
 
-template <typename T, int D, bool L2>
-__global__ void __launch_bounds__(kWarps * 32, blocks_per_sm<T, D, L2>()) conv_backward_kernel(ConvBwdParams p)
+// FULL: all kMaxWidth taps. With fewer the missing ones are skipped, not multiplied by zero: an infinite input
+// reaches no row beyond the width.
+template <typename T, int D, bool L2, bool FULL>
+__global__ void __launch_bounds__(kWarps * 32, blocks_per_sm<D>()) conv_backward_kernel(ConvBwdParams p)
 {
     constexpr int V = D / 32, P = V / 2, kLast = kMaxWidth - 1;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -95,6 +97,7 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm<T, D, L2>()) conv_b
     const T *dy = static_cast<const T *>(p.dy) + (size_t)n * p.T * HD + col;
     T *dx = static_cast<T *>(p.dx) + (size_t)n * p.T * HD + col;
     const size_t srow = (size_t)n * (p.W - 1);
+    const int skip = FULL ? 0 : kMaxWidth - p.W;
 
     f32x2 wt[kMaxWidth][P];  // right-aligned: wt[i] multiplies the input kLast - i back
 #pragma unroll
@@ -175,9 +178,10 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm<T, D, L2>()) conv_b
                     to_pairs<T, V>(gy[k + b], g[b]);
 #pragma unroll
                     for (int v = 0; v < P; ++v) {
-                        f32x2 a = mul2(wt[0][v], xw[k + b][v]);
+                        f32x2 a = mul2(wt[kLast][v], xw[k + b + kLast][v]);
 #pragma unroll
-                        for (int i = 1; i < kMaxWidth; ++i) a = fma2(wt[i][v], xw[k + b + i][v], a);
+                        for (int i = kLast - 1; i >= 0; --i)
+                            if (i >= skip) a = fma2(wt[i][v], xw[k + b + i][v], a);
                         float lo, hi;
                         split(a, lo, hi);
                         u[b][v] = a;
@@ -215,19 +219,22 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm<T, D, L2>()) conv_b
                 if constexpr (L2) ds = mul2(pair(inv[b], inv[b]), fma2(mul2(u[b][v], s), pair(f[b], f[b]), ds));
                 du[v] = mul2(ds, slope);
             }
-            if (!INNER && L2 && j >= p.T)
+            if (!INNER && j >= p.T)  // (its slope may be that of an infinite window)
 #pragma unroll
                 for (int v = 0; v < P; ++v) du[v] = 0;
             if (INNER || j < t1)
 #pragma unroll
                 for (int v = 0; v < P; ++v)
 #pragma unroll
-                    for (int i = 0; i < kMaxWidth; ++i) dw[i][v] = fma2(du[v], xw[k + i][v], dw[i][v]);
+                    for (int i = 0; i < kMaxWidth; ++i)
+                        if (i >= skip) dw[i][v] = fma2(du[v], xw[k + i][v], dw[i][v]);
 #pragma unroll
             for (int v = 0; v < P; ++v)
 #pragma unroll
-                for (int i = 0; i < kMaxWidth; ++i)
-                    dxp[(k + i) % 4][v] = i == kLast ? mul2(wt[i][v], du[v]) : fma2(wt[i][v], du[v], dxp[(k + i) % 4][v]);
+                for (int i = 0; i < kMaxWidth; ++i) {
+                    if (i == kLast) dxp[(k + i) % 4][v] = mul2(wt[i][v], du[v]);
+                    else if (i >= skip) dxp[(k + i) % 4][v] = fma2(wt[i][v], du[v], dxp[(k + i) % 4][v]);
+                }
             const int t = j - kLast;  // its row is finished
             if constexpr (INNER) {
                 store_pairs<T, V>(out, dxp[k]);
@@ -295,8 +302,10 @@ cudaError_t launch(const ConvBwdParams &p, bool l2, float *dweight, cudaStream_t
 {
     const long long tasks = (long long)p.N * p.H * p.runs;
     const unsigned blocks = (unsigned)((tasks + kWarps - 1) / kWarps);
-    if (l2) conv_backward_kernel<T, D, true><<<blocks, kWarps * 32, 0, st>>>(p);
-    else conv_backward_kernel<T, D, false><<<blocks, kWarps * 32, 0, st>>>(p);
+    const bool full = p.W == kMaxWidth;
+    auto *kern = l2 ? full ? conv_backward_kernel<T, D, true, true> : conv_backward_kernel<T, D, true, false>
+                    : full ? conv_backward_kernel<T, D, false, true> : conv_backward_kernel<T, D, false, false>;
+    kern<<<blocks, kWarps * 32, 0, st>>>(p);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     const long long values = (long long)p.H * D * kMaxWidth;
@@ -311,7 +320,7 @@ int run_of(int N, int T, int H, int d)
 {
     int dev = 0, sms = 148;
     if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    const long long slots = (long long)(sms > 0 ? sms : 148) * (d == 64 ? 4 : 3) * kWarps;
+    const long long slots = (long long)(sms > 0 ? sms : 148) * (d == 64 ? blocks_per_sm<64>() : blocks_per_sm<128>()) * kWarps;
     int best = 8;
     long long least = -1;
     for (int run = 8; run <= 256; run += run < 32 ? 4 : 16) {

@@ -249,7 +249,6 @@ __global__ void __launch_bounds__(kThreads, 2) head_norm_kernel(const __grid_con
                 if constexpr (BACKWARD) {
                     f32x2 ya[2], yb[2], dot = 0;
                     Row::get(row_at(stage, HB + k), ya, yb);
-                    if (h0 + k >= h1) ya[0] = ya[1] = yb[0] = yb[1] = 0;
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {  // turned back
                         ga[k][i] = fma2(yb[i], sn[i], mul2(ya[i], cs[i]));
@@ -293,8 +292,10 @@ __global__ void __launch_bounds__(kThreads, 2) head_norm_kernel(const __grid_con
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         const f32x2 va = mul2(a[k][i], inv2), vb = mul2(b[k][i], inv2);
-                        acca[i] = fma2(ga[k][i], va, acca[i]);
-                        accb[i] = fma2(gb[k][i], vb, accb[i]);
+                        if (h < h1) {  // a head read again may hold infinities, which zero would not clear
+                            acca[i] = fma2(ga[k][i], va, acca[i]);
+                            accb[i] = fma2(gb[k][i], vb, accb[i]);
+                        }
                         oa[i] = mul2(inv2, fma2(va, f2, mul2(ga[k][i], wa[i])));
                         ob[i] = mul2(inv2, fma2(vb, f2, mul2(gb[k][i], wb[i])));
                     }

@@ -178,6 +178,51 @@ def test_norm_of_huge_and_tiny_rows_and_zero_eps():
     assert g["dq"][0, 1, 0].isnan().all() and g["dq"][0, 0].isfinite().all() and g["dq"][0, 2].isfinite().all()
 
 
+@pytest.mark.parametrize("l2", [True, False])
+def test_an_infinite_input_stays_within_the_convolutions_width(l2):
+    """W = 2: u_j and u_{j+1} take x_j, so dx changes at j - 1, j and j + 1 only (with the norm, of its head only)."""
+    N, T, H, d, W, j = 1, 40, 2, 64, 2, 20
+    x, w, _ = I.make_conv_inputs((N, T, H, d), W, torch.float32, seed=38)
+    dy = torch.randn(x.shape, generator=torch.Generator().manual_seed(10)).cuda()
+    clean = gdr2_short_conv_silu_backward(x.cuda(), w.cuda(), dy, l2norm=l2)
+    for at in (j, T - 1):
+        bad = x.clone()
+        bad[0, at, 1, 5] = float("inf")
+        g = gdr2_short_conv_silu_backward(bad.cuda(), w.cuda(), dy, l2norm=l2)
+        gdr2_sync_status()
+        same = [t for t in range(T) if t not in (at - 1, at, at + 1)]
+        assert torch.equal(g["dx"][0, same], clean["dx"][0, same])
+        assert torch.equal(g["dx"][0, :, 0], clean["dx"][0, :, 0])
+        assert torch.equal(g["dweight"][:d], clean["dweight"][:d])
+
+
+def test_an_infinite_head_stays_in_its_channels_gradient():
+    """Without a norm the weight's gradient takes x itself: infinite in that channel, the same elsewhere. 17
+    heads leave tasks that read a head again, and few tokens groups that read a token again."""
+    q = torch.randn((1, 3, 17, 64), generator=torch.Generator().manual_seed(11)).cuda()
+    w, dy = torch.ones(64, device="cuda"), torch.rand_like(q) + 0.5
+    clean = gdr2_head_norm_rope_backward(q, None, dy, q_weight=w, norm=None)
+    q[0, 2, 16, 7] = float("inf")
+    g = gdr2_head_norm_rope_backward(q, None, dy, q_weight=w, norm=None)
+    gdr2_sync_status()
+    rest = [i for i in range(64) if i != 7]
+    assert g["dq_weight"][7] == float("inf") and torch.equal(g["dq_weight"][rest], clean["dq_weight"][rest])
+
+
+def test_a_given_stream_owns_what_the_call_allocates():
+    v = cuda(make((2, 300), 64, 16, torch.float32, 39, states=2))
+    want = gdr2_ssm_scan(**v)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    for _ in range(20):  # scratch of one call, freed at its end, is not handed to the current stream's tensors
+        got = gdr2_ssm_scan(**v, stream=s)
+        junk = torch.full((1 << 18,), float("nan"), device="cuda")
+    s.synchronize()
+    torch.cuda.synchronize()
+    gdr2_sync_status()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and junk.isnan().all()
+
+
 def test_two_streams_at_once():
     """Calls on two streams with buffers of their own do not touch each other."""
     v = cuda(make((1, 500), 96, 16, torch.bfloat16, 37, states=1))
