@@ -12,9 +12,12 @@
 // One pass over x and dy (u is formed again), one write of dx: an HBM stream of three
 // tensors. A warp walks one head over a run of tokens, four loads in flight. Of two tokens at a time the head's
 // two sums are taken by one butterfly that halves the four values with each step (10 shuffles instead of 20);
-// the last inputs and the unfinished dx rows stay in registers, pairs of channels in one 64-bit register each. It forms du for the W - 1 tokens after its run too, which its last dx
-// rows need. The weights' gradient is summed in registers over the run, then over runs and
+// the last inputs and the unfinished dx rows stay in registers, pairs of channels in one 64-bit register each. It
+// forms du for the W - 1 tokens after its run too, which its last dx rows need. The weights' gradient is summed in registers over the run, then over runs and
 // sequences by a second kernel in a fixed order.
+//
+// What bounds it: 34 instructions per element, at half an instruction per cycle from 12 warps: 68 us for 4 x 4096
+// tokens of 16 heads of 128 channels in bf16 with the norm (3.0 TB/s; the three tensors' HBM time is 31 us).
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

@@ -1,6 +1,6 @@
 // seq_ops.h -- device helpers of the layers around the mixer (selective scan, convolution
-// backward, head norm): runs of consecutive elements held as raw words, and the
-// elementwise laws in fp32.
+// backward, head norm): runs of consecutive elements held as raw words, pairs of fp32 values,
+// asynchronous copies, and the elementwise laws in fp32.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -57,22 +57,6 @@ template <typename T, int E> struct Raw {
             for (int i = 0; i < kWords; ++i) w[i] = __ldg(reinterpret_cast<const uint32_t *>(row) + min(c + i, last));
         }
     }
-    // the first `valid` elements one by one, zeros behind them
-    __device__ __forceinline__ void load_each(const T *p, int valid)
-    {
-        if constexpr (sizeof(T) == 2) {
-            const unsigned short *u = reinterpret_cast<const unsigned short *>(p);
-#pragma unroll
-            for (int i = 0; i < kWords; ++i) {
-                const uint32_t lo = 2 * i < valid ? __ldg(u + 2 * i) : 0u;
-                const uint32_t hi = 2 * i + 1 < valid ? __ldg(u + 2 * i + 1) : 0u;
-                w[i] = lo | (hi << 16);
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < kWords; ++i) w[i] = i < valid ? __ldg(reinterpret_cast<const uint32_t *>(p) + i) : 0u;
-        }
-    }
 };
 
 // bf16 pair, a in the low half
@@ -114,12 +98,6 @@ template <typename T, int E> __device__ __forceinline__ void store_each(T *p, co
     for (int i = 0; i < E; ++i)
         if (i < valid) store_one(p + i, v[i]);
 }
-template <typename T> __device__ __forceinline__ float load_one(const T *p)
-{
-    if constexpr (sizeof(T) == 2) return __bfloat162float(*p);
-    else return *p;
-}
-
 // One element as raw bits, so that a load in flight is not waited for, and its value.
 template <typename T> __device__ __forceinline__ uint32_t load_bits(const T *p)
 {

@@ -11,15 +11,15 @@
 // What bounds it: one exponential per (token, channel, state) on the special-function unit, 16 per
 // SM and cycle, and four for a (token, channel) (softplus and the gate): at N = 16 a floor of 172 us for 4 x 4096
 // tokens of 2048 channels, against 41 us of HBM traffic. The single-token step reads and
-// writes its state and is bound by HBM.
+// writes its state and is bound by HBM (20.5 us for 256 x 2048 x 16 states, 3.5 TB/s).
 //
 // Work split: a block owns 32 channels over a segment of the time axis, in tiles of 32 tokens. N / 4
 // scanning warps hold four states of each channel in registers, lane = channel: B and C are
 // broadcast reads of shared memory, no shuffles, and a token costs a warp 4 exponentials and about 17
 // other instructions. Four helper warps do what is done once per (token, channel): step sizes
 // ahead of the scan, and behind it the sum of the warps' parts, the skip and the gate. (Lanes of one
-// channel side by side, each token's work in the same threads, took 587 us; this form 248 us with
-// two blocks per SM, 69% of the floor; helpers alone 127 us, scanning warps alone 162 us.)
+// channel side by side, each token's work in the same threads, took 587 us; this form 254 us with
+// two blocks per SM, 68% of the floor; helpers alone 127 us, scanning warps alone 162 us.)
 //
 // Where the channels do not fill the GPU the time axis is cut in g segments: a first launch scans the
 // first segment whole and gives the others' final states from zero and the sums of their
@@ -537,8 +537,8 @@ cudaError_t launch_step_n(int N, const StepParams &p, cudaStream_t st)
 
 // Segments of the time axis. With one the scan is a single launch of a block per 32 channels; with
 // g > 2 two launches of g - 1 blocks per 32 channels, each over T / g tokens. A token costs an SM that runs k blocks,
-// two at a time, k units, and a block that is alone kAlone (at N = 16: 30 ns a unit, 38 ns alone).
-SsmSplit ssm_scan_split(int streams, int T, int D, int N)
+// two at a time, k units, and a block that is alone kAlone (at N = 16: 31 ns a unit, 39 ns alone).
+SsmSplit ssm_scan_split(int streams, int T, int D)
 {
     constexpr double kAlone = 1.27;
     const long long blocks = (long long)streams * ((D + kCh - 1) / kCh);
@@ -562,7 +562,7 @@ SsmSplit ssm_scan_split(int streams, int T, int D, int N)
 
 size_t ssm_scan_workspace_bytes(int streams, int T, int D, int N)
 {
-    const SsmSplit s = ssm_scan_split(streams, T, D, N);
+    const SsmSplit s = ssm_scan_split(streams, T, D);
     if (s.nseg <= 1) return 0;
     const size_t n = (size_t)streams * s.nseg * D;
     return (n * (N + 1) * sizeof(float) + 255) / 256 * 256;
@@ -572,7 +572,7 @@ cudaError_t launch_ssm_scan(const SsmArgs &a, cudaStream_t st)
 {
     const int streams = a.cu_seqlens ? 1 : a.B;
     if (a.T > 0 && streams > 0 && a.D > 0) {
-        const SsmSplit s = ssm_scan_split(streams, a.T, a.D, a.N);
+        const SsmSplit s = ssm_scan_split(streams, a.T, a.D);
         ScanParams p;
         p.T = a.T; p.D = a.D; p.nseq = a.B;
         p.seg = s.seg; p.nseg = s.nseg;
