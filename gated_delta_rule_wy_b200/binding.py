@@ -53,6 +53,8 @@ _lib = None
 def load_library(path: str | None = None) -> ctypes.CDLL:
     """Load libgdr2.so once and declare the signatures of include/gdr2.h."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -159,26 +161,27 @@ def _one_device(fn):
     """
     @functools.wraps(fn)
     def call(*args, **kwargs):
-        dev = None
-        for group in (args, kwargs.values()):
-            for a in group:
+        stream = kwargs.get("stream")
+        if stream is None:  # the common call: all tensors on the current device
+            index = current = torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -1
+            for a in (*args, *kwargs.values()):
                 if isinstance(a, torch.Tensor):
-                    if dev is None:
-                        dev = a.device
-                    elif a.device != dev:
-                        _device_of(_tensors_in(args, kwargs))
+                    index = a.get_device()
+                    if index != current:
+                        break
                 elif isinstance(a, (list, tuple)):
-                    dev = _device_of(_tensors_in(args, kwargs))
+                    index = -1
+                    break
+            if index == current >= 0:
+                return fn(*args, **kwargs)
+        dev = _device_of(_tensors_in(args, kwargs))
         if dev is None or dev.type != "cuda":
             return fn(*args, **kwargs)  # the argument checks reject host tensors
-        stream = kwargs.get("stream")
         if stream is not None and stream.device != dev:
             raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}: one CUDA device per call")
         if stream is not None:
             with torch.cuda.stream(stream):
                 return fn(*args, **kwargs)
-        if torch.cuda.current_device() == dev.index:
-            return fn(*args, **kwargs)
         with torch.cuda.device(dev):
             return fn(*args, **kwargs)
     return call
@@ -191,7 +194,7 @@ def _ptr(t):
 def _stream(stream=None):
     """The raw stream, the current one of the current device unless one is given."""
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return stream.cuda_stream
 
 
@@ -478,7 +481,7 @@ def gdr2_short_conv_silu_backward(x, weight, dy, state=None, dstate_out=None, *,
     g = {"dx": torch.empty_like(x), "dweight": _like(weight), "dstate": x.new_empty((N, W - 1, H, d)) if want else None}
     if N * H == 0:
         g["dweight"].zero_()
-    need = lib.gdr2_short_conv_silu_backward_workspace_bytes(N, T, H, d, W)
+    need = _scratch("gdr2_short_conv_silu_backward_workspace_bytes", x.device.index, N, T, H, d, W)
     workspace = _workspace(workspace, need, x.device)
     st = lib.gdr2_short_conv_silu_backward(N, T, H, d, _dt(x), W, int(bool(l2norm)), eps, _some(x),
                                            _some(wgt), _some(state), _some(dy), _some(dstate_out), _some(g["dx"]),
@@ -500,6 +503,12 @@ def _nbytes(t):
 def _like(t):
     """An uninitialised contiguous tensor of t's shape, dtype and device."""
     return torch.empty_like(t) if t.is_contiguous() else t.new_empty(t.shape)
+
+
+@functools.lru_cache(maxsize=1024)
+def _scratch(query, device, *sizes):
+    """The bytes that the library's `query` asks for: a function of the sizes and of the (current) device alone."""
+    return getattr(load_library(), query)(*sizes)
 
 
 def _workspace(given, need, device):
@@ -530,6 +539,15 @@ def _rows(t, name, lead, width, dtype):
     return _row_distance(name, lead, strides, width)
 
 
+def _ld(t, name, shape, dtype):
+    """_rows of a tensor of `shape`, without a call or a tuple where it is contiguous."""
+    if t is None:
+        return 0
+    if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
+        return shape[-1]
+    return _rows(t, name, tuple(shape[:-1]), shape[-1], dtype)
+
+
 def _row_distance(name, lead, strides, width):
     """The one distance between rows of `width` elements over the leading dimensions, or a refusal."""
     ld, rows = None, 1  # distance between rows; the rows that the dimensions from here on hold
@@ -550,14 +568,17 @@ def _row_distance(name, lead, strides, width):
 def _ssm_inputs(x, dt, A, Bm, Cm, D, z, dt_bias, packed=None):
     """Checks the inputs that the scan, its step and its backward share; returns their sizes
     and the C arguments x .. step_bias."""
-    lead, C = tuple(x.shape[:-1]), x.shape[-1]
+    shape, t = x.shape, x.dtype
+    lead, C = tuple(shape[:-1]), shape[-1]
     N = A.shape[-1]
-    t = x.dtype
-    ldx, ldt = _rows(x, "x", lead, C, t), _rows(dt, "dt", lead, C, t)
-    ldb, ldc, ldz = _rows(Bm, "Bm", lead, N, t), _rows(Cm, "Cm", lead, N, t), _rows(z, "z", lead, C, t)
+    states = (*lead, N)
+    ldx, ldt, ldz = _ld(x, "x", shape, t), _ld(dt, "dt", shape, t), _ld(z, "z", shape, t)
+    ldb, ldc = _ld(Bm, "Bm", states, t), _ld(Cm, "Cm", states, t)
     _check(A, "A", (C, N), torch.float32)
-    _check(D, "D", (C,), torch.float32)
-    _check(dt_bias, "dt_bias", (C,), torch.float32)
+    if D is not None:
+        _check(D, "D", (C,), torch.float32)
+    if dt_bias is not None:
+        _check(dt_bias, "dt_bias", (C,), torch.float32)
     if packed is not None:
         _check_cu_seqlens(packed, x.device)
     args = (_some(x), ldx, _some(dt), ldt, _some(A), _some(Bm), ldb, _some(Cm), ldc, _some(D), _some(z), ldz,
@@ -591,7 +612,7 @@ def gdr2_ssm_scan(x, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, S0=None, *, so
     if save_states and cu_seqlens is not None:
         raise ValueError("save_states is for dense sequences (the backward takes no cu_seqlens)")
     saved = A.new_empty((B, -(-T // SSM_CHUNK), C, N)) if save_states else None
-    need = lib.gdr2_ssm_scan_workspace_bytes(B if cu_seqlens is None else 1, T, C, N)
+    need = _scratch("gdr2_ssm_scan_workspace_bytes", dev.index, B if cu_seqlens is None else 1, T, C, N)
     workspace = _workspace(workspace, need, dev)
     st = lib.gdr2_ssm_scan(B, T, C, N, _dt(x), int(bool(softplus)), _ptr(cu_seqlens), *args, _some(S0), _some(y),
                            _some(S_T), _some(saved), _some(workspace), _nbytes(workspace), _stream(stream))
@@ -634,7 +655,7 @@ def gdr2_ssm_scan_backward(x, dt, A, Bm, Cm, dy, D=None, z=None, dt_bias=None, S
          "dD": None if D is None else _like(D), "dz": None if z is None else _like(z),
          "ddt_bias": None if dt_bias is None else _like(dt_bias),
          "dS0": A.new_empty((B, C, N)) if want_dS0 else None}
-    need = lib.gdr2_ssm_scan_backward_workspace_bytes(B, T, C, N, int(saved_states is not None))
+    need = _scratch("gdr2_ssm_scan_backward_workspace_bytes", dev.index, B, T, C, N, int(saved_states is not None))
     workspace = _workspace(workspace, need, dev)
     st = lib.gdr2_ssm_scan_backward(B, T, C, N, _dt(x), int(bool(softplus)), *args, _some(S0), _some(dy), _some(dS_T),
                                     _some(saved_states), *(_some(g[k]) for k in ("dx", "ddt", "dA", "dBm", "dCm", "dD",
