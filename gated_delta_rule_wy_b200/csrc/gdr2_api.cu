@@ -525,7 +525,7 @@ gdr2_status gdr2_ssm_scan(int B, int T, int D, int N, gdr2_dtype dt, int softplu
     if (has_tokens && (y == x || y == step || y == z))
         return fail(GDR2_ERR_INVALID_ARG, "y must not be x, step or z");
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (!has_tokens && !cu_seqlens) {
+    if (!has_tokens) {
         if (!S_T) return GDR2_OK;
         const size_t bytes = (size_t)B * D * N * sizeof(float);
         return launched(S0 ? cudaMemcpyAsync(S_T, S0, bytes, cudaMemcpyDeviceToDevice, s)

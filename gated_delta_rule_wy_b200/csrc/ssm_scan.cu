@@ -93,6 +93,18 @@ __device__ __forceinline__ void scan_segment(const ScanParams &p, int g, float *
     const int tbeg = g * p.seg, tend = min(p.T, tbeg + p.seg);
     const int nt = (tend - tbeg + kTile - 1) / kTile;
 
+    if (!SUMMARY && p.cu && g == 0 && p.S_T)  // packed sequences without tokens keep their state, or get zeros
+        for (int s = warp; s < p.nseq; s += S::kBlock / 32) {
+            if (__ldg(p.cu + s) != __ldg(p.cu + s + 1)) continue;
+            for (int i = lane; i < kCh * N / 4; i += 32) {
+                const int c = c0 + i / (N / 4);
+                const size_t at = ((size_t)s * p.D + c) * N + i % (N / 4) * 4;
+                if (c < p.D)
+                    *reinterpret_cast<float4 *>(p.S_T + at) =
+                        p.S0 ? *reinterpret_cast<const float4 *>(p.S0 + at) : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+        }
+
     if (warp < G) {  // ---------------------------------------------------------------- scan
         const int c = c0 + lane, q = warp;
         const bool live = c < p.D;
@@ -244,6 +256,7 @@ __device__ __forceinline__ void scan_segment(const ScanParams &p, int g, float *
             }
         }
     };
+    int seq_begin = 0x7fffffff, seq_end = 0;
     // the fetched tile into buffer `buf`; tokens past the segment and channels past D are inert
     // (D = 0: the decay is 1 and nothing is added)
     auto convert = [&](const Tokens &tok, int t0, int buf) {
@@ -277,11 +290,15 @@ __device__ __forceinline__ void scan_segment(const ScanParams &p, int g, float *
         if (p.cu && hid < 32) {  // packed: which of the tile's tokens begin and end a sequence
             const int t = t0 + hid;
             bool first = false, last = false;
-            if (t < tend) {
-                const int s = find_sequence(p.cu, p.nseq, t);
+            if (!(seq_begin < t0 && t0 + kTile < seq_end)) {  // not all of the tile inside the sequence last seen
+                const int s = find_sequence(p.cu, p.nseq, min(t, tend - 1));
                 sseq[buf][hid] = s;
-                first = __ldg(p.cu + s) == t;
-                last = __ldg(p.cu + s + 1) == t + 1;
+                seq_begin = __ldg(p.cu + s);
+                seq_end = __ldg(p.cu + s + 1);
+                first = t < tend && seq_begin == t;
+                last = t < tend && seq_end == t + 1;
+                seq_begin = __shfl_sync(0xffffffffu, seq_begin, 31);  // of the tile's last token
+                seq_end = __shfl_sync(0xffffffffu, seq_end, 31);
             }
             const unsigned mf = __ballot_sync(0xffffffffu, first), ml = __ballot_sync(0xffffffffu, last);
             if (hid == 0) { smask[buf][0] = mf; smask[buf][1] = ml; }
@@ -367,14 +384,6 @@ __global__ void __launch_bounds__(ScanShape<N>::kBlock, ScanShape<N>::kBlocks) s
     } else {
         scan_segment<T, N, VEC, false>(p, p.nseg > 1 ? blockIdx.y + 1 : 0, smem, smask, sseq);
     }
-}
-
-// Packed sequences without tokens keep their state (or get zeros): one block per sequence.
-__global__ void ssm_empty_kernel(const int *cu, const float *S0, float *S_T, size_t n)
-{
-    const int s = blockIdx.x;
-    if (__ldg(cu + s) != __ldg(cu + s + 1)) return;
-    for (size_t i = threadIdx.x; i < n; i += blockDim.x) S_T[s * n + i] = S0 ? S0[s * n + i] : 0.f;
 }
 
 // ---------------------------------------------------------------- one token
@@ -587,10 +596,6 @@ cudaError_t launch_ssm_scan(const SsmArgs &a, cudaStream_t st)
         p.dsum = p.hloc + (size_t)streams * s.nseg * a.D * a.N;
         const cudaError_t e = a.bf16 ? launch_scan_n<__nv_bfloat16>(a, p, st) : launch_scan_n<float>(a, p, st);
         if (e != cudaSuccess) return e;
-    }
-    if (a.cu_seqlens && a.S_T && a.B > 0 && a.D > 0) {
-        ssm_empty_kernel<<<a.B, 256, 0, st>>>(a.cu_seqlens, a.S0, a.S_T, (size_t)a.D * a.N);
-        return cudaGetLastError();
     }
     return cudaSuccess;
 }

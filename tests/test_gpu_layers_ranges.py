@@ -101,6 +101,24 @@ def test_long_packed_sequences_across_segments(lens):
     check_scan(v, y, S_T, [(slice(ends[i], ends[i + 1]), i, lens[i]) for i in range(n) if lens[i]])
 
 
+@pytest.mark.parametrize("states", [True, False])
+def test_many_empty_sequences_keep_their_states(states):
+    """Among tokens, behind the last one, and alone."""
+    C, N = 45, 8
+    for lens in ([0] * 37 + [3] + [0] * 50 + [40, 0, 0], [0] * 5):
+        T, n = sum(lens), len(lens)
+        v = make((T,), C, N, torch.float32, 40, states=n)
+        if not states:
+            v["S0"] = None
+        ends = np.concatenate([[0], np.cumsum(lens)])
+        y, S_T, _ = gdr2_ssm_scan(**cuda(v), cu_seqlens=torch.tensor(ends, dtype=torch.int32, device="cuda"))
+        gdr2_sync_status()
+        check_scan(v, y, S_T, [(slice(ends[i], ends[i + 1]), i, lens[i]) for i in range(n) if lens[i]])
+        for i in range(n):
+            if not lens[i]:
+                assert torch.equal(S_T[i].cpu(), v["S0"][i] if states else torch.zeros(C, N))
+
+
 def test_what_is_not_finite_stays_in_its_sequence():
     """A NaN or an infinity in one packed sequence, or one batch entry, reaches no other; the last
     token's, which padded tiles read again, reaches no earlier token."""
