@@ -11,7 +11,7 @@
 // What bounds it: one exponential per (token, channel, state) on the special-function unit, 16 per
 // SM and cycle, and four for a (token, channel) (softplus and the gate): at N = 16 a floor of 172 us for 4 x 4096
 // tokens of 2048 channels, against 41 us of HBM traffic. The single-token step reads and
-// writes its state and is bound by HBM (20.5 us for 256 x 2048 x 16 states, 3.5 TB/s).
+// writes its state and is bound by HBM (18.7 us for 256 x 2048 x 16 states, 3.8 TB/s).
 //
 // Work split: a block owns 32 channels over a segment of the time axis, in tiles of 32 tokens. N / 4
 // scanning warps hold four states of each channel in registers, lane = channel: B and C are
@@ -402,7 +402,7 @@ struct StepParams {
 // lanes: lane q loads x, step and z of sequence q, forms its step size and finishes its output. Loads
 // are never conditional: sequences past B and channels past D read the last one and store nothing.
 template <typename T, int N, int SEQS>
-__global__ void __launch_bounds__(kThreads) ssm_step_kernel(StepParams p)
+__global__ void __launch_bounds__(kThreads, 8) ssm_step_kernel(StepParams p)
 {
     constexpr int L = N / 4, CH = kThreads / L;
     constexpr int OWN = SEQS <= L ? 1 : SEQS / L;  // sequences a lane does the channel's work of
@@ -520,12 +520,13 @@ cudaError_t launch_scan_n(const SsmArgs &a, const ScanParams &p, cudaStream_t st
 template <typename T, int N>
 cudaError_t launch_step(const StepParams &p, cudaStream_t st)
 {
-    // Four sequences per thread where that leaves two blocks per SM, else one, for latency.
-    // (256 sequences of 2048 channels, N = 16, bf16: 18.8 us, with one per thread 22.4; one of 1000 channels, fp32: 3.8 us, with four 4.1.)
+    // Two sequences per thread where that leaves two blocks per SM, else one, for latency. (256 sequences of 2048
+    // channels, N = 16, bf16: 18.7 us with two per thread and eight blocks per SM, 18.8 to 20.7 with four and four, 22.4 with
+    // one; one sequence of 1000 channels, fp32: 3.8 us with one per thread, 4.1 with four.)
     constexpr int per = kThreads / (N / 4);
     const unsigned cb = (unsigned)((p.D + per - 1) / per);
-    if ((long long)((p.B + 3) / 4) * cb >= 2LL * sm_count())
-        ssm_step_kernel<T, N, 4><<<(unsigned)((p.B + 3) / 4) * cb, kThreads, 0, st>>>(p);
+    if ((long long)((p.B + 1) / 2) * cb >= 2LL * sm_count())
+        ssm_step_kernel<T, N, 2><<<(unsigned)((p.B + 1) / 2) * cb, kThreads, 0, st>>>(p);
     else
         ssm_step_kernel<T, N, 1><<<(unsigned)p.B * cb, kThreads, 0, st>>>(p);
     return cudaGetLastError();

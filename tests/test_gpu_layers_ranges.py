@@ -154,7 +154,7 @@ def test_what_is_not_finite_stays_in_its_sequence():
 @pytest.mark.parametrize("N", [8, 16, 32, 64])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_single_tokens_of_many_sequences_are_those_of_few(dtype, N):
-    """403 sequences are stepped four to a thread, a few one to a thread: the same operations on each."""
+    """403 sequences are stepped several to a thread, a few one to a thread: the same operations on each."""
     B, C = 403, 520
     v = make((B,), C, N, dtype, 35, states=B)
     d = cuda(v)
