@@ -145,15 +145,15 @@ __device__ __forceinline__ float rcp(float x)  // 1 / x, one unit in the last pl
 constexpr float kDecayBias = 3.0e-8f;
 __device__ __forceinline__ float decay2(float d, float a2) { return ex2(fmaf(d, a2, kDecayBias)); }
 
-// e^x with the rounding of x log2 e, which grows with |x|, put back: the product's error is exact in a fused
-// multiply-add, and the rest of log2 e's digits are a second constant. (Beyond |x| = 80 it is left out: there it
-// would be infinity times zero.)
+// e^x for x <= 0 with the rounding of x log2 e, which grows with |x|, put back: the product's error is exact in a
+// fused multiply-add, and the rest of log2 e's digits are a second constant. (Below x = -104, where the value is 0,
+// it is left out: for an infinite x it is infinity minus infinity.)
 __device__ __forceinline__ float exp_rest(float x)
 {
     constexpr float kLog2eRest = 1.925963e-8f, kLn2 = 0.69314718f;
     const float y = x * kLog2e, rest = fmaf(x, kLog2eRest, fmaf(x, kLog2e, -y));
     const float e = ex2(y);
-    return fmaf(e * kLn2, fabsf(x) < 80.f ? rest : 0.f, e);
+    return fmaf(e * kLn2, x < -104.f ? 0.f : rest, e);
 }
 
 // log(1 + e^v) = max(v, 0) + log(1 + e), e = e^-|v| in (0, 1], with log(1 + e) = 2 atanh(s),
@@ -172,7 +172,13 @@ __device__ __forceinline__ float softplus(float v)
 }
 // 1 / (1 + e^-v); below v = -88 the exponential overflows and the quotient is 0
 __device__ __forceinline__ float sigmoid(float v) { return rcp(1.f + ex2(-v * kLog2e)); }
-__device__ __forceinline__ float softplus_slope(float v) { return rcp(1.f + exp_rest(-v)); }
+// the same without an exponential above 1: a step of any size below zero, infinite ones too, has a slope of 0, not
+// the quotient of an infinity
+__device__ __forceinline__ float softplus_slope(float v)
+{
+    const float e = exp_rest(-fabsf(v));
+    return (v < 0.f ? e : 1.f) * rcp(1.f + e);
+}
 
 // Two fp32 values in one 64-bit register, and the instructions that work on both at once.
 typedef unsigned long long f32x2;
