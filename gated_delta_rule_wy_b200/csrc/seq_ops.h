@@ -216,6 +216,20 @@ __device__ __forceinline__ f32x2 ex2x2(f32x2 v)
     split(v, lo, hi);
     return pair(ex2(lo), ex2(hi));
 }
+// 2^(d a) h + o for two states: a value carried over a segment whose step sizes sum to d, and the segment's own part.
+// The factor alone may pass fp32's range where the product does not (h zero or small before growth, large before
+// decay): it is then applied in four parts, each held to 2^-126 .. 2^127. The limits change no result: four such
+// factors take every nonzero h (2^-149 at least) to infinity, and every finite one to zero. NaN takes the first way.
+__device__ __forceinline__ f32x2 carry2(float d, float a, float b, f32x2 h, f32x2 o)
+{
+    const float x = d * a, y = d * b;
+    if (!(fmaxf(fabsf(x), fabsf(y)) > 125.f)) return fma2(pair(decay2(d, a), decay2(d, b)), h, o);
+    auto quarter = [](float v) { return ex2(fminf(fmaxf(0.25f * v, -126.f), 127.f)); };
+    const f32x2 q = pair(quarter(x), quarter(y));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h = mul2(q, h);
+    return add2(h, o);
+}
 // 16 bytes of shared memory as two pairs
 __device__ __forceinline__ void lds_pairs(const float *p, f32x2 &a, f32x2 &b)
 {

@@ -160,7 +160,7 @@ __device__ __forceinline__ void walk_segment(const BwdParams &p, int g, float *s
                     f32x2 o[2];
                     load_state(p.eloc, at, r, o);
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) e[r][k] = fma2(decay(ds, r, k), e[r][k], o[k]);
+                    for (int k = 0; k < 2; ++k) e[r][k] = carry2(ds, A2[r][2 * k], A2[r][2 * k + 1], e[r][k], o[k]);
                 }
             }
         }

@@ -144,7 +144,7 @@ __device__ __forceinline__ void scan_segment(const ScanParams &p, int g, float *
                     f32x2 o[2];
                     load_state(p.hloc, at, o);
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) h[k] = fma2(decay(ds, k), h[k], o[k]);
+                    for (int k = 0; k < 2; ++k) h[k] = carry2(ds, A2[2 * k], A2[2 * k + 1], h[k], o[k]);
                 }
             }
         }

@@ -77,3 +77,43 @@ def test_masked_steps_among_ordinary_ones(dtype, step, N):
     check_gradients(v, dy, dS, g, T)
     for b, t in ((0, 17), (1, T - 1)):
         assert not g["ddt"][b, t].any()
+
+
+@pytest.mark.parametrize("N", [8, 16, 32, 64])
+def test_growth_over_a_segment_leaves_zero(N):
+    """A > 0: 32 steps grow by e^256, which fp32 does not hold. The state is zero until the last three tokens, and the
+    state's gradient zero after the first three, so that nothing that is there grows: all is finite, as token by token."""
+    T, C = 2000, 33
+    v = make((1, T), C, N, torch.float32, 410, z=False, bias=False)
+    v.update(A=torch.full((C, N), 8.0), dt=torch.ones((1, T, C)))
+    v["x"][:, :-3] = 0.0
+    dy = torch.randn((1, T, C), generator=torch.Generator().manual_seed(43))
+    dy[:, 3:] = 0.0
+    y, S_T, _ = gdr2_ssm_scan(**cuda(v), softplus=False)
+    g = backward(v, dy, softplus=False)
+    gdr2_sync_status()
+    for name, t in (("y", y), ("S_T", S_T), *g.items()):
+        assert t is None or t.isfinite().all(), name
+    check_scan(v, y, S_T, [((0,), 0, T)], with_softplus=False)
+    check_gradients(v, dy, None, g, T, with_softplus=False)
+    assert not g["dS0"][..., 0].eq(0).all()
+
+
+@pytest.mark.parametrize("sign", [1, -1])
+def test_a_factor_beyond_fp32_whose_product_is_not(sign):
+    """Exponents that sum to 130 (of 2) over 32 tokens in the middle, and steps of zero elsewhere: the state of 2^-125
+    ends at 32, the one of 2^125 at 2^-5, wherever the segments' borders fall. The same for the state's gradient.
+
+    One step: 2^x 4 U, its exponent 4 (2 U) and the product 1 U; the tokens' 32 steps, or one factor's four parts."""
+    T, C, N = 2048, 40, 16
+    A = torch.full((C, N), sign * 130 / 32 * 0.6931471805599453, device="cuda")
+    n, x = torch.zeros((1, T, N), device="cuda"), torch.zeros((1, T, C), device="cuda")
+    dt = torch.zeros((1, T, C), device="cuda")
+    dt[:, T // 2:T // 2 + 32] = 1.0
+    S0 = torch.full((1, C, N), 2.0 ** (-125 * sign), device="cuda")
+    _, S_T, _ = gdr2_ssm_scan(x, dt, A, n, n, S0=S0, softplus=False)
+    g = gdr2_ssm_scan_backward(x, dt, A, n, n, x, S0=torch.zeros_like(S0), dS_T=S0, softplus=False)
+    gdr2_sync_status()
+    want = np.exp(np64(A)[None] * 32) * np64(S0)
+    for got in (S_T, g["dS0"]):
+        assert np.all(np.abs(np64(got) - want) <= 32 * 16 * U * want)
