@@ -4,6 +4,7 @@
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+#include <float.h>
 #include <stdint.h>
 
 namespace gdr2 {
@@ -144,6 +145,11 @@ __device__ __forceinline__ float rcp(float x)  // 1 / x, one unit in the last pl
 // in the exponent takes that out. It leaves 2^0 = 1 as it is.
 constexpr float kDecayBias = 3.0e-8f;
 __device__ __forceinline__ float decay2(float d, float a2) { return ex2(fmaf(d, a2, kDecayBias)); }
+
+// A for use by the kernels, and as the rate a2 of decay2. An A of minus infinity counts as the lowest finite value, so that
+// a step of 0, as those that fill up a tile are, leaves the state (infinity times 0 is NaN) and any other clears it.
+__device__ __forceinline__ float held(float a) { return a < -FLT_MAX ? -FLT_MAX : a; }
+__device__ __forceinline__ float decay_rate(float a) { return held(a * kLog2e); }
 
 // e^x for x <= 0 with the rounding of x log2 e, which grows with |x|, put back: the product's error is exact in a
 // fused multiply-add, and the rest of log2 e's digits are a second constant. (Below x = -104, where the value is 0,

@@ -144,8 +144,9 @@ __device__ __forceinline__ void walk_segment(const BwdParams &p, int g, float *s
             for (int k = 0; k < 2; ++k) {
                 float lo, hi;
                 split(A[r][k], lo, hi);
-                A2[r][2 * k] = lo * kLog2e;
-                A2[r][2 * k + 1] = hi * kLog2e;
+                A[r][k] = pair(held(lo), held(hi));
+                A2[r][2 * k] = decay_rate(lo);
+                A2[r][2 * k + 1] = decay_rate(hi);
             }
             // e = a_{t+1} dh_{t+1}, the gradient that enters this segment from the right
             if (!live) continue;

@@ -112,7 +112,7 @@ __device__ __forceinline__ void scan_segment(const ScanParams &p, int g, float *
         f32x2 h[2] = {0, 0};
         if (live) {
             const float4 a = *reinterpret_cast<const float4 *>(p.A + (size_t)c * N + 4 * q);
-            A2[0] = a.x * kLog2e; A2[1] = a.y * kLog2e; A2[2] = a.z * kLog2e; A2[3] = a.w * kLog2e;
+            A2[0] = decay_rate(a.x); A2[1] = decay_rate(a.y); A2[2] = decay_rate(a.z); A2[3] = decay_rate(a.w);
         }
         auto load_state = [&](const float *base, size_t index, f32x2 (&v)[2]) {
             const float4 a = *reinterpret_cast<const float4 *>(base + (index * p.D + c) * N + 4 * q);
@@ -431,7 +431,7 @@ __global__ void __launch_bounds__(kThreads, 8) ssm_step_kernel(StepParams p)
         rz[o] = p.z ? load_bits(static_cast<const T *>(p.z) + seq * p.ldz + c) : 0u;
     }
     float4 a = __ldg(reinterpret_cast<const float4 *>(p.A + (size_t)c * N + 4 * q));
-    a.x *= kLog2e; a.y *= kLog2e; a.z *= kLog2e; a.w *= kLog2e;
+    a.x = decay_rate(a.x); a.y = decay_rate(a.y); a.z = decay_rate(a.z); a.w = decay_rate(a.w);
     const float bias = p.bias ? __ldg(p.bias + c) : 0.f, skip = p.Dskip ? __ldg(p.Dskip + c) : 0.f;
     float d[OWN], x[OWN];
 #pragma unroll

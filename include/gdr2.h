@@ -308,7 +308,8 @@ gdr2_status gdr2_gate_activations(gdr2_dtype dt, long long n_alpha, const void *
  *   step_bias [D] fp32; states [B][D][N] fp32. The pointers of A, the states, saved_states and the
  *   workspace are 16-byte aligned, all others aligned to their element.
  * Sizes: N is 8, 16, 32 or 64 (GDR2_ERR_UNSUPPORTED otherwise); B, T, D >= 0, any D. Arithmetic
- *   and states are fp32; A may have either sign; nothing is clamped.
+ *   and states are fp32; A may have either sign; nothing is clamped, but that an A of minus infinity
+ *   counts as the lowest finite value (a step of 0 leaves its state, any other clears it).
  */
 #define GDR2_SSM_CHUNK 16 /* tokens between the saved states of gdr2_ssm_scan */
 

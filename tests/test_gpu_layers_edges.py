@@ -3,7 +3,7 @@ import numpy as np
 import pytest
 import torch
 
-from gated_delta_rule_wy_b200 import gdr2_ssm_scan, gdr2_ssm_scan_backward, gdr2_sync_status
+from gated_delta_rule_wy_b200 import gdr2_ssm_scan, gdr2_ssm_scan_backward, gdr2_ssm_step, gdr2_sync_status
 from layer_bounds import U, np64
 from oracle import layers as OL
 from test_gpu_ssm import backward, check_gradients, check_scan, cuda, make
@@ -117,3 +117,31 @@ def test_a_factor_beyond_fp32_whose_product_is_not(sign):
     want = np.exp(np64(A)[None] * 32) * np64(S0)
     for got in (S_T, g["dS0"]):
         assert np.all(np.abs(np64(got) - want) <= 32 * 16 * U * want)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("T", [1, 16, 41, 64, 1500])
+def test_states_that_forget_at_every_step(dtype, T):
+    """An A of minus infinity: h_t = s_t B_t x_t alone, whether the last tile is full or not, and no gradient passes a
+    token or reaches A. A finite one of the same effect gives the same."""
+    C, N = 40, 16
+    v = make((2, T), C, N, dtype, 420 + T, states=2)
+    v["A"][:, ::3] = -float("inf")
+    w = {**v, "A": v["A"].nan_to_num(neginf=-1e6)}
+    dy = torch.randn((2, T, C), generator=torch.Generator().manual_seed(44)).to(dtype)
+    dS = torch.randn((2, C, N), generator=torch.Generator().manual_seed(45))
+    y, S_T, saved = gdr2_ssm_scan(**cuda(v), save_states=True)
+    g, h = backward(v, dy, dS, saved_states=saved), backward(w, dy, dS)
+    y2, S2, _ = gdr2_ssm_scan(**cuda(w))
+    gdr2_sync_status()
+    assert torch.equal(y, y2) and torch.equal(S_T, S2)
+    assert all(torch.equal(g[k], h[k]) for k in g)
+    check_scan(w, y, S_T, [((b,), b, T) for b in range(2)])
+    check_gradients(w, dy, dS, g, T)
+    S = v["S0"].cuda()
+    d = cuda({k: t[:, 0].contiguous() if k in ("x", "dt", "Bm", "Cm", "z") else t for k, t in v.items() if k != "S0"})
+    gdr2_ssm_step(**d, S=S)
+    gdr2_sync_status()
+    step = (torch.nn.functional.softplus(d["dt"].double() + d["dt_bias"].double()) * d["x"].double())[..., None]
+    want = (step * d["Bm"].double()[:, None, :])[..., ::3]
+    assert ((S[..., ::3].double() - want).abs() <= 96 * U * want.abs()).all()
