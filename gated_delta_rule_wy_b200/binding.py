@@ -141,6 +141,15 @@ def _tensors_in(args, kwargs):
             yield from (x for x in a if isinstance(x, torch.Tensor))
 
 
+def _tensors_of(result):
+    """The tensors that a call returns, one by one or in tuples and dicts."""
+    if isinstance(result, torch.Tensor):
+        yield result
+    elif isinstance(result, (tuple, list, dict)):
+        for part in result.values() if isinstance(result, dict) else result:
+            yield from _tensors_of(part)
+
+
 def _device_of(tensors):
     """The one device the tensors live on (None without tensors); raises if they span several."""
     devs = {t.device for t in tensors}
@@ -157,7 +166,8 @@ def _one_device(fn):
     device would reach kernels as foreign pointers: the call is made under that device
     (its current stream unless one is given), after checking that every tensor argument
     and the stream share it. A given stream is the current one during the call, so that outputs and
-    scratch are allocated in its order.
+    scratch are allocated in its order; the caller's own stream, on which outputs are read later, is recorded
+    as a user of them, so that their memory is not handed to the given stream's next call before it has read them.
     """
     @functools.wraps(fn)
     def call(*args, **kwargs):
@@ -180,8 +190,13 @@ def _one_device(fn):
         if stream is not None and stream.device != dev:
             raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}: one CUDA device per call")
         if stream is not None:
+            caller = torch.cuda.current_stream(dev)
             with torch.cuda.stream(stream):
-                return fn(*args, **kwargs)
+                result = fn(*args, **kwargs)
+            if caller != stream:
+                for t in _tensors_of(result):
+                    t.record_stream(caller)
+            return result
         with torch.cuda.device(dev):
             return fn(*args, **kwargs)
     return call
