@@ -17,7 +17,7 @@ from __future__ import annotations
 import torch
 import torch.distributed as dist
 
-from .binding import gdr2_forward, gdr2_segment_states
+from .binding import _one_device, gdr2_forward, gdr2_segment_states
 
 
 def _transition_inputs(v, w, dk):
@@ -31,6 +31,7 @@ def _identity(n, H, dk, device):
     return torch.eye(dk, dtype=torch.float32, device=device).expand(n, H, dk, dk).contiguous()
 
 
+@_one_device
 def gdr2_forward_segmented(q, k, v, log_alpha, b, w, S0=None, *, segments, final_state=True, stream=None):
     """gdr2_forward with each sequence cut into ``segments`` equal parts run side by side on
     one GPU. Inputs as gdr2_forward ([B, T, H, .], T a multiple of ``segments``). Returns

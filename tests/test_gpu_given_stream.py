@@ -2,7 +2,8 @@
 import pytest
 import torch
 
-from gated_delta_rule_wy_b200 import gdr2_ssm_scan, gdr2_sync_status
+from gated_delta_rule_wy_b200 import gdr2_forward_segmented, gdr2_ssm_scan, gdr2_sync_status
+from gated_delta_rule_wy_b200 import inputs as I
 from test_gpu_ssm import cuda, make
 
 pytestmark = pytest.mark.gpu
@@ -52,3 +53,23 @@ def test_a_given_stream_inside_a_capture():
         torch.cuda.synchronize()
         assert torch.equal(y2, want[0]) and torch.equal(S2, want[1])
         assert torch.equal(again[0], want[0]) and torch.equal(again[1], want[1])
+
+
+def test_segmented_forward_makes_its_own_inputs_on_the_given_stream():
+    """The zero and identity inputs of the segments' transitions are made where they are read: not behind what the
+    caller's stream still has to do, and not in memory that its tensors get back."""
+    x = I.make_forward_inputs(B=1, H=2, T=512, dk=128, dv=128, dtype=torch.bfloat16, decay_shift=2.0, seed=145,
+                              with_S0=True).to("cuda")
+    args = (x.q, x.k, x.v, x.log_alpha, x.b, x.w, x.S0)
+    want = gdr2_forward_segmented(*args, segments=4)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        torch.cuda._sleep(50_000_000)
+        o, S_T = gdr2_forward_segmented(*args, segments=4, stream=s)
+        junk = [torch.full((n,), float("nan"), device="cuda") for n in (1 << 15, 1 << 17, 1 << 20)]
+        s.synchronize()
+        assert torch.equal(o, want[0]) and torch.equal(S_T, want[1])
+    torch.cuda.synchronize()
+    gdr2_sync_status()
+    assert all(t.isnan().all() for t in junk)
