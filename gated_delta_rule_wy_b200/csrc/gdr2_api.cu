@@ -447,7 +447,9 @@ gdr2_status gdr2_short_conv_silu_backward(int N, int T, int H, int d, gdr2_dtype
     if (width < 1 || width > 4) return fail(GDR2_ERR_UNSUPPORTED, "width must be 1 .. 4 (width=%d)", width);
     if (l2norm != 0 && l2norm != 1) return fail(GDR2_ERR_INVALID_ARG, "l2norm must be 0 or 1");
     GDR2_TRY(check_eps(l2_eps, "l2_eps"));
-    if ((long long)N * T * H * d > (1ll << 40)) return fail(GDR2_ERR_INVALID_ARG, "problem too large");
+    // in floating point, where products do not wrap; the limits hold both launches' grids below 2^31 blocks
+    if ((double)N * (T > 0 ? T : 1) * H * d > 0x1p38 || (double)H * d > 0x1p33)
+        return fail(GDR2_ERR_INVALID_ARG, "problem too large");
     if ((long long)N * H == 0) return GDR2_OK;
     const bool has_tokens = T > 0;
     GDR2_TRY(check_ptr(x, "x", !has_tokens));

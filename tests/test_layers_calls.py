@@ -1,0 +1,27 @@
+"""Calls of the layers around the mixer whose sizes pass the integers that carry them (no GPU needed)."""
+import ctypes
+
+import pytest
+
+import gated_delta_rule_wy_b200 as g
+from gated_delta_rule_wy_b200 import binding as b
+
+P, Q, S = (ctypes.c_void_p(v) for v in (0x10000, 0x20000, 0x30000))
+MOST = 2 ** 31 - 1
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from gated_delta_rule_wy_b200 import build
+
+    build.build()
+    return g.load_library()
+
+
+@pytest.mark.parametrize("N,T,H", [(1 << 21, 1 << 21, 1 << 21), (MOST, MOST, MOST), (MOST, 0, MOST), (1 << 20, 0, 1 << 20),
+                                   (1, 1, MOST), (1 << 24, 1 << 10, 1 << 10)])
+def test_convolution_gradients_refuse_sizes_whose_products_wrap(lib, N, T, H):
+    """Elements, scratch bytes or blocks past their integers, also where a product of them is a small number again."""
+    st = lib.gdr2_short_conv_silu_backward(N, T, H, 64, b.GDR2_BF16, 4, 0, ctypes.c_float(1e-6), P, P, None, Q, None, S, S,
+                                           None, P, ctypes.c_size_t((1 << 64) - 1), None)
+    assert st == b.GDR2_ERR_INVALID_ARG and b"too large" in lib.gdr2_last_error()
