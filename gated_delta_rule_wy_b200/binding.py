@@ -705,6 +705,8 @@ def _head_rows(v, name, shape, dtype):
 def _rope_inputs(q, k, q_weight, k_weight, cos_sin, positions, norm, eps, interleaved, first_position):
     if norm not in _NORMS:
         raise ValueError(f"norm must be 'rms', 'l2' or None, not {norm!r}")
+    if not -2 ** 31 <= first_position < 2 ** 31:  # a C int would take its low 32 bits
+        raise ValueError(f"first_position {first_position} does not fit into 32 bits")
     B, T, Hq, d = q.shape
     Hk = 0 if k is None else k.shape[2]
     t = q.dtype

@@ -25,3 +25,14 @@ def test_convolution_gradients_refuse_sizes_whose_products_wrap(lib, N, T, H):
     st = lib.gdr2_short_conv_silu_backward(N, T, H, 64, b.GDR2_BF16, 4, 0, ctypes.c_float(1e-6), P, P, None, Q, None, S, S,
                                            None, P, ctypes.c_size_t((1 << 64) - 1), None)
     assert st == b.GDR2_ERR_INVALID_ARG and b"too large" in lib.gdr2_last_error()
+
+
+def test_a_first_position_past_32_bits_is_not_taken_for_its_low_half():
+    import torch
+
+    q = torch.zeros(1, 4, 2, 64)
+    for first in (2 ** 31, 2 ** 32 + 3, -2 ** 31 - 1, -2 ** 32 + 3):
+        with pytest.raises(ValueError, match="first_position"):
+            g.gdr2_head_norm_rope(q, first_position=first)
+        with pytest.raises(ValueError, match="first_position"):
+            g.gdr2_head_norm_rope_backward(q, None, q, first_position=first)
