@@ -628,6 +628,8 @@ gdr2_status gdr2_head_norm_rope(int B, int T, int Hq, int Hk, int d, gdr2_dtype 
         if (outs[i] == q || outs[i] == k) return fail(GDR2_ERR_INVALID_ARG, "%s must not be q or k", names[i]);
         a.side[i].out = outs[i];
     }
+    if (a.side[0].out && a.side[0].out == a.side[1].out)
+        return fail(GDR2_ERR_INVALID_ARG, "q_out and k_out must not be the same buffer");
     GDR2_TRY(device_status(&a.status));
     return launched(gdr2::launch_head_norm_rope(a, static_cast<cudaStream_t>(stream)), "gdr2_head_norm_rope");
 }
@@ -664,6 +666,8 @@ gdr2_status gdr2_head_norm_rope_backward(int B, int T, int Hq, int Hk, int d, gd
         a.side[i].dy = in[i];
         a.side[i].out = outs[i];
     }
+    if ((a.side[0].out && a.side[0].out == a.side[1].out) || (dq_weight && dq_weight == dk_weight))
+        return fail(GDR2_ERR_INVALID_ARG, "the gradients of q and k must not be the same buffer");
     if (!dq_weight && !dk_weight && (!has_tokens || Hq + Hk == 0)) return GDR2_OK;
     GDR2_TRY(check_workspace(workspace, workspace_bytes, gdr2::head_norm_backward_workspace_bytes(d), 16));
     a.workspace = workspace;

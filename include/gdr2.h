@@ -380,7 +380,7 @@ gdr2_status gdr2_ssm_scan_backward(int B, int T, int D, int N, gdr2_dtype dt, in
  *      positions [B * T] int32, DEVICE memory, or NULL: token t of every sequence is at
  *      first_position + t. A position outside 0 .. P - 1 leaves its token unturned, and the next
  *      gdr2_sync_status returns GDR2_ERR_INVALID_ARG.
- * out: q_out [B * T][Hq][d], k_out [B * T][Hk][d], contiguous; they must not overlap an input.
+ * out: q_out [B * T][Hq][d], k_out [B * T][Hk][d], contiguous; they must not overlap each other or an input.
  * d is 64, 128 or 256; R a multiple of 16, at most d; eps finite and >= 0; q, k, the outputs and
  * cos_sin are 16-byte aligned, ldq and ldk whole multiples of 16 bytes.
  */
@@ -400,7 +400,8 @@ size_t gdr2_head_norm_rope_backward_workspace_bytes(int d);
 /*
  * gdr2_head_norm_rope_backward -- its gradients: dq [B * T][Hq][d] and dk from q, k (the
  *   forward's inputs) and dq_out, dk_out (contiguous, the outputs' layout); dq_weight, dk_weight [d] fp32 or
- *   NULL (not wanted), summed in a fixed order. scratch: 16-byte aligned.
+ *   NULL (not wanted), summed in a fixed order. scratch: 16-byte aligned. Output buffers must not overlap
+ *   each other or an input.
  */
 gdr2_status gdr2_head_norm_rope_backward(int B, int T, int Hq, int Hk, int d, gdr2_dtype dt, int norm, float eps,
                                          const void *q, long long ldq, const void *k, long long ldk,

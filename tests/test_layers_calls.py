@@ -36,3 +36,11 @@ def test_a_first_position_past_32_bits_is_not_taken_for_its_low_half():
             g.gdr2_head_norm_rope(q, first_position=first)
         with pytest.raises(ValueError, match="first_position"):
             g.gdr2_head_norm_rope_backward(q, None, q, first_position=first)
+
+
+def test_norm_and_rotation_refuse_one_buffer_for_both_outputs(lib):
+    common = (1, 4, 2, 2, 64, b.GDR2_BF16, 1, ctypes.c_float(1e-6), P, 128, P, 128, None, None, 64, 0, P, 16, None, 0)
+    assert lib.gdr2_head_norm_rope(*common, Q, Q, None) == b.GDR2_ERR_INVALID_ARG and b"same" in lib.gdr2_last_error()
+    for dq, dk, dqw, dkw in ((Q, Q, None, None), (Q, S, ctypes.c_void_p(0x50000), ctypes.c_void_p(0x50000))):
+        st = lib.gdr2_head_norm_rope_backward(*common, P, P, dq, dk, dqw, dkw, P, ctypes.c_size_t(1 << 40), None)
+        assert st == b.GDR2_ERR_INVALID_ARG and b"same" in lib.gdr2_last_error()
