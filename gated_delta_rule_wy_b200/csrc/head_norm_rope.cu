@@ -31,7 +31,8 @@ using namespace seq;
 constexpr int kThreads = 256;
 constexpr int kMaxBlocks = 1024;  // of the backward: one partial weight gradient each, and one for the other side
 constexpr int kStages = 3;  // tasks whose copies are under way, one of them at hand
-// heads per task: what their registers allow at two blocks per SM
+// heads per task: what their registers allow at two blocks per SM. (bf16 runs two; in fp32 three stages of rows are 120 KB of
+// shared memory a block, so that one runs at a time and a grid for two takes two rounds.)
 constexpr int heads_per_task(bool backward) { return backward ? 2 : 4; }
 
 struct Side {

@@ -615,8 +615,9 @@ int sm_count()
 }
 
 // Segments of the time axis, as in the forward. Of two launches the first runs a whole segment and g - 2 summaries
-// per 32 channels, the second g - 1 whole ones; a summary costs kSummary of a whole token.
-SsmSplit ssm_backward_split(int streams, int T, int D, int N)
+// per 32 channels, the second g - 1 whole ones; a summary costs kSummary of a whole token. The constants are those of
+// N = 16, two blocks per SM; the other N take the same rule, which was not measured for them.
+SsmSplit ssm_backward_split(int streams, int T, int D)
 {
     constexpr double kAlone = 1.27, kSummary = 0.45;
     const long long blocks = (long long)streams * ((D + kCh - 1) / kCh);
@@ -648,7 +649,7 @@ struct Layout {
 };
 Layout layout(int B, int T, int D, int N, bool have_saved)
 {
-    const SsmSplit s = ssm_backward_split(B, T, D, N);
+    const SsmSplit s = ssm_backward_split(B, T, D);
     const size_t ncb = (size_t)(D + kCh - 1) / kCh, parts = (size_t)B * s.nseg;
     const size_t nchunk = (size_t)(T + kSsmChunk - 1) / kSsmChunk;
     size_t at = 0;
@@ -689,7 +690,7 @@ cudaError_t launch_ssm_backward(const SsmArgs &a, const SsmGrads &g, cudaStream_
         if (e != cudaSuccess) return e;
         saved = f.saved_states;
     }
-    const SsmSplit s = ssm_backward_split(a.B, a.T, a.D, a.N);
+    const SsmSplit s = ssm_backward_split(a.B, a.T, a.D);
     BwdParams p;
     p.B = a.B; p.T = a.T; p.D = a.D; p.seg = s.seg; p.nseg = s.nseg;
     p.nchunk = (a.T + kSsmChunk - 1) / kSsmChunk;

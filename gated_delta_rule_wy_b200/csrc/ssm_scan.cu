@@ -11,7 +11,8 @@
 // What bounds it: one exponential per (token, channel, state) on the special-function unit, 16 per
 // SM and cycle, and four for a (token, channel) (softplus and the gate): at N = 16 a floor of 172 us for 4 x 4096
 // tokens of 2048 channels, against 41 us of HBM traffic. The single-token step reads and
-// writes its state and is bound by HBM (18.7 us for 256 x 2048 x 16 states, 3.8 TB/s).
+// writes its state (18.7 us for 256 x 2048 x 16 states, 3.8 TB/s, 58% of the HBM rate): 58 warps per SM
+// issue in 64% of the cycles, much of it for B and C, read element by element, and wait for loads 58% of their time.
 //
 // Work split: a block owns 32 channels over a segment of the time axis, in tiles of 32 tokens. N / 4
 // scanning warps hold four states of each channel in registers, lane = channel: B and C are
@@ -547,7 +548,8 @@ cudaError_t launch_step_n(int N, const StepParams &p, cudaStream_t st)
 
 // Segments of the time axis. With one the scan is a single launch of a block per 32 channels; with
 // g > 2 two launches of g - 1 blocks per 32 channels, each over T / g tokens. A token costs an SM that runs k blocks,
-// two at a time, k units, and a block that is alone kAlone (at N = 16: 31 ns a unit, 39 ns alone).
+// two at a time, k units, and a block that is alone kAlone (at N = 16: 31 ns a unit, 39 ns alone; within 5% of the best of
+// nine counts tried there). N = 32 and 64 run one block per SM and take the same rule, which was not measured for them.
 SsmSplit ssm_scan_split(int streams, int T, int D)
 {
     constexpr double kAlone = 1.27;

@@ -86,7 +86,9 @@ typedef enum {
 #define GDR2_GATE_SCALAR_B 1
 #define GDR2_GATE_SCALAR_W 2
 
-/* ABI version of the loaded library (GDR2_ABI_VERSION it was built with). */
+/* ABI version of the loaded library (GDR2_ABI_VERSION it was built with). The layers around the mixer
+ * (gdr2_short_conv_silu_backward, gdr2_ssm_*, gdr2_head_norm_rope*) were added under version 9, which
+ * libraries without them report too: a program that loads either looks up the symbol. */
 int gdr2_abi_version(void);
 
 /* Human-readable description of the calling thread's last non-OK status
