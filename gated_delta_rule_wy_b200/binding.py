@@ -609,7 +609,8 @@ def gdr2_ssm_scan(x, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, S0=None, *, so
     h_t = exp(s_t A) h_{t-1} + s_t Bm_t x_t with s_t = softplus(dt_t + dt_bias) (softplus=False:
     dt_t + dt_bias); y_t = (Cm_t . h_t + D x_t) * silu(z_t).
     x, dt, z: [B, T, C]; Bm, Cm: [B, T, N] (one dtype, fp32 or bf16; views of fused projections
-    keep their row stride); with cu_seqlens (int32 [B + 1]) [T, .], packed. A: [C, N], D, dt_bias:
+    keep their row stride); with cu_seqlens (int32 [B + 1], nondecreasing from 0 to T; not checked: other values give
+    unspecified outputs) [T, .], packed. A: [C, N], D, dt_bias:
     [C], S0, S_T: [B, C, N] fp32; N is 8, 16, 32 or 64. saved_states, when asked for (dense):
     [B, ceil(T / 16), C, N], for gdr2_ssm_scan_backward.
     """
